@@ -257,6 +257,103 @@ dsa_status hisa_index(const dsa_batch* batch, const void* Q, const void* K, cons
                       int32_t* kept, void* ws, size_t ws_bytes, void* stream);
 
 /* --------------------------------------------------------------------
+ * Operators an indexer is trained with.  ("ADIndex: Layer-Adaptive Sparse
+ * Attention Indexing via Group-Level Distillation", abstract, trains group
+ * indexers by distillation; the pages give no formulas.  The loss is the
+ * one DeepSeek-V3.2's indexer is trained with: the divergence of the
+ * indexer's distribution over a list of keys from the main attention's.)
+ * One training step of an indexer is
+ *     K = dsa_layer_norm(projected keys); lists = dsa_index_topk(...);
+ *     scores = dsa_list_scores(lists);
+ *     loss, dscores = dsa_distill_topk(scores, teacher);
+ *     dQ, dK, dW = dsa_list_scores_backward(dscores);
+ *     dx, dweight, dbias = dsa_layer_norm_backward(dK).
+ * Every sum is kept in fp32 and taken in an order that depends on the sizes
+ * alone: the same call gives the same bits.  Rows and matrices are only
+ * touched inside their stated extent.
+ */
+enum { DSA_BF16 = 0, DSA_FP32 = 1 };                          /* element types */
+enum { DSA_TEACHER_LOGITS = 0, DSA_TEACHER_WEIGHTS = 1 };     /* what a teacher's values are */
+
+/* --------------------------------------------------------------------
+ * Layer norm of n rows of d values: y = (x - mean) rstd weight + bias with
+ * rstd = 1 / sqrt(var + eps), var the biased variance; statistics in fp32
+ * (two passes over registers).  Rows are ld_* elements apart (>= d; any
+ * alignment of the element type: rows on 16-byte boundaries with d a multiple
+ * of 8 take wide loads), so x may be a column slice of a wider projection.
+ * x_type, y_type: DSA_BF16 or DSA_FP32, independently.  weight, bias [d] fp32
+ * or NULL (ones, zeros); mean, rstd [n] fp32 or NULL.  y may be x's own
+ * memory when types and strides agree.  1 <= d <= 16384.
+ */
+dsa_status dsa_layer_norm(int64_t n, int32_t d, const void* x, int32_t x_type, int64_t ld_x, const float* weight,
+                          const float* bias, float eps, void* y, int32_t y_type, int64_t ld_y, float* mean,
+                          float* rstd, void* stream);
+
+/* Its backward pass from the forward's mean and rstd: dx (x's type; NULL:
+ * not wanted), dweight and dbias [d] fp32 (NULL: not wanted).  With
+ * xh = (x - mean) rstd and g = dy weight:
+ *     dx = rstd (g - mean(g) - xh mean(g xh)), dweight = sum dy xh, dbias = sum dy.
+ * n = 0 leaves dweight and dbias zero.  dx may be dy's or x's own memory when
+ * types and strides agree.
+ */
+size_t dsa_layer_norm_backward_workspace(int64_t n, int32_t d);
+dsa_status dsa_layer_norm_backward(int64_t n, int32_t d, const void* dy, int32_t dy_type, int64_t ld_dy,
+                                   const void* x, int32_t x_type, int64_t ld_x, const float* weight,
+                                   const float* mean, const float* rstd, void* dx, int64_t ld_dx, float* dweight,
+                                   float* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/* --------------------------------------------------------------------
+ * Distillation of a row's scores from a teacher's top logits or weights:
+ * loss and gradient in one pass.  n rows of k places (k >= 1, any length).
+ * scores fp32; lists int32 or NULL; teacher DSA_BF16 or DSA_FP32; rows ld_*
+ * elements apart.  A place counts when its list entry is not negative (lists
+ * given) and its score is above -inf: rows of dsa_list_scores, or whole rows
+ * of dsa_index_scores with no lists.  What stands in places that do not
+ * count (NaN, infinities) has no effect.  Over the counted places
+ *     q = softmax(scores / temperature),
+ *     p = softmax(teacher / temperature)     (DSA_TEACHER_LOGITS; -inf: p = 0)
+ *       = teacher / sum(teacher)             (DSA_TEACHER_WEIGHTS; >= 0),
+ *     loss[r] = sum p (log p - log q),
+ *     dscores = grad_loss[r] / temperature * (q - p), 0 in places that do not count.
+ * grad_loss [n] or NULL (ones); loss [n] or NULL; dscores or NULL, which may
+ * be scores' own memory with the same stride.  A row with no counted place,
+ * or none that the teacher gives weight, has loss 0 and gradient 0.
+ */
+dsa_status dsa_distill_topk(int32_t n, int32_t k, const float* scores, int64_t ld_scores, const int32_t* lists,
+                            int64_t ld_lists, const void* teacher, int32_t teacher_type, int64_t ld_teacher,
+                            int32_t teacher_kind, float temperature, const float* grad_loss, float* loss,
+                            float* dscores, int64_t ld_dscores, void* stream);
+
+/* --------------------------------------------------------------------
+ * Indexer scores at listed keys.  lists [n_q, k] int32 (device, read only):
+ * query t's keys, sequence-local indices, strictly ascending, then -1 padding
+ * (the rows dsa_index_topk, PIVOT and HISA return; or a teacher's own top
+ * keys).  scores [n_q, k] fp32: I[t, lists[t][j]] for listed keys of the
+ * query's prefix (s <= q_pos[t]), -inf in every other place.  A list that is
+ * not ascending, holds a key outside its sequence or has a key after its
+ * padding is used up to its first bad entry and reported through the
+ * workspace status word (code 2, read with dsa_device_check).
+ * Requires 1 <= k <= 16384.
+ */
+size_t dsa_list_scores_workspace(const dsa_batch* batch, int32_t k);
+dsa_status dsa_list_scores(const dsa_batch* batch, const void* Q, const void* K, const float* W, int32_t k,
+                           const int32_t* lists, float* scores, void* ws, size_t ws_bytes, void* stream);
+
+/* Their backward pass: from dscores [n_q, k] fp32 (read only where a score is
+ * above -inf) the gradients dQ [n_q, H, d] bf16, dK [n_k, d] bf16 and dW
+ * [n_q, H] fp32, each NULL when not wanted, written whole (zeros where nothing
+ * is listed):
+ *     dW[t,h] = sum_j dscores[t,j] max(0, q[t,h] . k),
+ *     G = dscores[t,j] w[t,h] where q[t,h] . k > 0 (else 0),
+ *     dQ[t,h] = sum_j G k,   dK[s] = sum over the (t, h) that list s of G q[t,h].
+ * dQ and dK 16-byte aligned.
+ */
+size_t dsa_list_scores_backward_workspace(const dsa_batch* batch, int32_t k);
+dsa_status dsa_list_scores_backward(const dsa_batch* batch, const void* Q, const void* K, const float* W, int32_t k,
+                                    const int32_t* lists, const float* dscores, void* dQ, void* dK, float* dW,
+                                    void* ws, size_t ws_bytes, void* stream);
+
+/* --------------------------------------------------------------------
  * Reads the workspace status word written by the kernels of earlier calls
  * on `stream` (synchronises the stream).  Returns DSA_OK when no kernel
  * recorded a problem, else DSA_ERR_DEVICE_CHECK and, if `detail` is not

@@ -9,8 +9,10 @@ when the compiled library is missing.
 
 Entry points mirror include/dsa_index.h:
   index_scores, index_topk, index_topk_host, index_layers, pivot_group_index,
-  pivot_refine_candidates, hisa_pool_keys, hisa_index, device_check, plus the
-  *_workspace size queries.
+  pivot_refine_candidates, hisa_pool_keys, hisa_index, device_check, the
+  operators an indexer is trained with (layer_norm, layer_norm_backward,
+  list_scores, list_scores_backward, distill_topk), plus the *_workspace
+  size queries.
 """
 from __future__ import annotations
 
@@ -34,6 +36,8 @@ _lib = ctypes.CDLL(LIB_PATH)
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported shape", 3: "workspace", 4: "CUDA error",
           5: "device check"}
 REUSE, REFINE = 0, 1
+BF16, FP32 = 0, 1                            # element types
+TEACHER_LOGITS, TEACHER_WEIGHTS = 0, 1       # what a teacher's values are
 
 
 class DsaError(RuntimeError):
@@ -86,6 +90,16 @@ _sig("dsa_index_layers_source", _I32, _I32, _I32, _I32)
 _sig("dsa_index_layers_workspace", _SZ, _B, _I32)
 _sig("dsa_index_layers", ctypes.c_int, _B, _I32, ctypes.POINTER(_P), ctypes.POINTER(_P), ctypes.POINTER(_P), _I32,
      _I32, _I32, ctypes.POINTER(_P), ctypes.POINTER(_P), _P, _SZ, _P, _P)
+_sig("dsa_layer_norm", ctypes.c_int, _I64, _I32, _P, _I32, _I64, _P, _P, ctypes.c_float, _P, _I32, _I64, _P, _P, _P)
+_sig("dsa_layer_norm_backward_workspace", _SZ, _I64, _I32)
+_sig("dsa_layer_norm_backward", ctypes.c_int, _I64, _I32, _P, _I32, _I64, _P, _I32, _I64, _P, _P, _P, _P, _I64, _P,
+     _P, _P, _SZ, _P)
+_sig("dsa_distill_topk", ctypes.c_int, _I32, _I32, _P, _I64, _P, _I64, _P, _I32, _I64, _I32, ctypes.c_float, _P, _P,
+     _P, _I64, _P)
+_sig("dsa_list_scores_workspace", _SZ, _B, _I32)
+_sig("dsa_list_scores", ctypes.c_int, _B, _P, _P, _P, _I32, _P, _P, _P, _SZ, _P)
+_sig("dsa_list_scores_backward_workspace", _SZ, _B, _I32)
+_sig("dsa_list_scores_backward", ctypes.c_int, _B, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P)
 _sig("dsa_profile_enable", None, _I32)
 _sig("dsa_launch_count", ctypes.c_uint64)
 _sig("dsa_profile_kind_name", ctypes.c_char_p, _I32)
@@ -343,6 +357,169 @@ def hisa_index(layout: Layout, Q, K, W, pooled, k: int, block: int, keep: int, i
                            _ptr(kept), _ptr(ws), _bytes(ws), _stream(stream)), "hisa_index")
     _after(ws, "hisa_index", stream)
     return (idx, kept) if want_kept else idx
+
+
+# ---------------------------------------------------------------- training
+
+_TYPES = {torch.bfloat16: BF16, torch.float32: FP32}
+
+
+def _rows(t, name, device, shape=None, dtype=None):
+    """A 2-D row matrix the library can read in place: unit stride along a row, on `device`."""
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name}: expected a 2-D tensor{'' if shape is None else f' of shape {shape}'}, "
+                         f"got {tuple(t.shape)}")
+    if t.dtype not in _TYPES if dtype is None else t.dtype != dtype:
+        raise ValueError(f"{name}: {t.dtype} is not supported here")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: values of a row must be adjacent")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: rows overlap")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _dense(t, name, device, shape, dtype):
+    """A contiguous tensor of the given shape and type on `device`; None passes."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _device(t):
+    """The CUDA device of a tensor, with an index (the library has no CPU path)."""
+    if not t.is_cuda:
+        raise ValueError("expected CUDA tensors")
+    return t.device
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, out_dtype=None, want_stats=False, stream=None):
+    """Layer norm of the rows of x [n, d] (bf16 or fp32; rows may be a slice of a wider matrix): y [n, d] of
+    out_dtype (x's by default); with want_stats also mean and rstd [n] fp32, which the backward pass takes."""
+    dev = _device(x)
+    ld_x = _rows(x, "x", dev)
+    n, d = x.shape
+    _dense(weight, "weight", dev, (d,), torch.float32)
+    _dense(bias, "bias", dev, (d,), torch.float32)
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty(n, d, dtype=out_dtype or x.dtype, device=dev)
+        ld_y = _rows(out, "out", dev, (n, d))
+        mean = rstd = None
+        if want_stats:
+            mean, rstd = torch.empty(2, n, dtype=torch.float32, device=dev).unbind(0)
+        _check(_lib.dsa_layer_norm(n, d, _ptr(x), _TYPES[x.dtype], ld_x, _ptr(weight), _ptr(bias), eps, _ptr(out),
+                                   _TYPES[out.dtype], ld_y, _ptr(mean), _ptr(rstd), _stream(stream)),
+               "dsa_layer_norm")
+    return (out, mean, rstd) if want_stats else out
+
+
+def layer_norm_backward_workspace(n: int, d: int) -> int:
+    return int(_lib.dsa_layer_norm_backward_workspace(n, d))
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, dx=None, ws=None, stream=None):
+    """Backward pass of layer_norm: (dx [n, d] of x's type, dweight [d], dbias [d] fp32)."""
+    dev = _device(x)
+    ld_x = _rows(x, "x", dev)
+    n, d = x.shape
+    ld_dy = _rows(dy, "dy", dev, (n, d))
+    _dense(weight, "weight", dev, (d,), torch.float32)
+    _dense(mean, "mean", dev, (n,), torch.float32)
+    _dense(rstd, "rstd", dev, (n,), torch.float32)
+    with torch.cuda.device(dev):
+        if dx is None:
+            dx = torch.empty(n, d, dtype=x.dtype, device=dev)
+        ld_dx = _rows(dx, "dx", dev, (n, d), x.dtype)
+        dw, db = torch.empty(2, d, dtype=torch.float32, device=dev).unbind(0)
+        ws = _workspace(layer_norm_backward_workspace(n, d), dev, ws)
+        _check(_lib.dsa_layer_norm_backward(n, d, _ptr(dy), _TYPES[dy.dtype], ld_dy, _ptr(x), _TYPES[x.dtype], ld_x,
+                                            _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx), ld_dx, _ptr(dw), _ptr(db),
+                                            _ptr(ws), _bytes(ws), _stream(stream)), "dsa_layer_norm_backward")
+    return dx, dw, db
+
+
+def distill_topk(scores, teacher, lists=None, kind: int = TEACHER_LOGITS, temperature: float = 1.0, grad_loss=None,
+                 loss=None, dscores=None, stream=None):
+    """Distillation loss of each row's scores [n, k] from a teacher's logits or weights on the same places, and
+    its gradient: (loss [n], dscores [n, k]).  Places with a negative entry in `lists` or a score of -inf do not
+    count.  grad_loss [n]: the gradient of each row's loss (ones by default)."""
+    dev = _device(scores)
+    ld_s = _rows(scores, "scores", dev, dtype=torch.float32)
+    n, k = scores.shape
+    ld_t = _rows(teacher, "teacher", dev, (n, k))
+    ld_l = 0 if lists is None else _rows(lists, "lists", dev, (n, k), torch.int32)
+    _dense(grad_loss, "grad_loss", dev, (n,), torch.float32)
+    with torch.cuda.device(dev):
+        if loss is None:
+            loss = torch.empty(n, dtype=torch.float32, device=dev)
+        if dscores is None:
+            dscores = torch.empty(n, k, dtype=torch.float32, device=dev)
+        _dense(loss, "loss", dev, (n,), torch.float32)
+        ld_d = _rows(dscores, "dscores", dev, (n, k), torch.float32)
+        _check(_lib.dsa_distill_topk(n, k, _ptr(scores), ld_s, _ptr(lists), ld_l, _ptr(teacher), _TYPES[teacher.dtype],
+                                     ld_t, kind, temperature, _ptr(grad_loss), _ptr(loss), _ptr(dscores), ld_d,
+                                     _stream(stream)), "dsa_distill_topk")
+    return loss, dscores
+
+
+def _list_inputs(layout, Q, K, W, lists):
+    dev = _device(Q)
+    H, d, n_q, n_k = layout.num_heads, layout.head_dim, layout.num_queries, layout.c.num_keys
+    if layout.q_off.device != dev:
+        raise ValueError(f"Q is on {dev}, the layout on {layout.q_off.device}")
+    _dense(Q, "Q", dev, (n_q, H, d), torch.bfloat16)
+    _dense(K, "K", dev, (n_k, d), torch.bfloat16)
+    _dense(W, "W", dev, (n_q, H), torch.float32)
+    if lists.dim() != 2:
+        raise ValueError("lists: expected [n_q, k]")
+    _dense(lists, "lists", dev, (n_q, lists.shape[1]), torch.int32)
+    return dev, n_q, int(lists.shape[1])
+
+
+def list_scores_workspace(layout: Layout, k: int) -> int:
+    return int(_lib.dsa_list_scores_workspace(layout.ref(), k))
+
+
+def list_scores(layout: Layout, Q, K, W, lists, scores=None, ws=None, stream=None):
+    """Indexer scores at listed keys: lists [n_q, k] int32 (ascending, -1 padded) -> scores [n_q, k] fp32, -inf
+    where a place is empty or its key is not in the query's prefix."""
+    dev, n_q, k = _list_inputs(layout, Q, K, W, lists)
+    with torch.cuda.device(dev):
+        if scores is None:
+            scores = torch.empty(n_q, k, dtype=torch.float32, device=dev)
+        _dense(scores, "scores", dev, (n_q, k), torch.float32)
+        ws = _workspace(list_scores_workspace(layout, k), dev, ws)
+        _check(_lib.dsa_list_scores(layout.ref(), _ptr(Q), _ptr(K), _ptr(W), k, _ptr(lists), _ptr(scores), _ptr(ws),
+                                    _bytes(ws), _stream(stream)), "dsa_list_scores")
+        _after(ws, "dsa_list_scores", stream)
+    return scores
+
+
+def list_scores_backward_workspace(layout: Layout, k: int) -> int:
+    return int(_lib.dsa_list_scores_backward_workspace(layout.ref(), k))
+
+
+def list_scores_backward(layout: Layout, Q, K, W, lists, dscores, dQ=None, dK=None, dW=None, ws=None, stream=None):
+    """Backward pass of list_scores: (dQ [n_q, H, d] bf16, dK [n_k, d] bf16, dW [n_q, H] fp32)."""
+    dev, n_q, k = _list_inputs(layout, Q, K, W, lists)
+    _dense(dscores, "dscores", dev, (n_q, k), torch.float32)
+    with torch.cuda.device(dev):
+        dQ = torch.empty_like(Q) if dQ is None else dQ
+        dK = torch.empty_like(K) if dK is None else dK
+        dW = torch.empty_like(W) if dW is None else dW
+        _dense(dQ, "dQ", dev, Q.shape, torch.bfloat16)
+        _dense(dK, "dK", dev, K.shape, torch.bfloat16)
+        _dense(dW, "dW", dev, W.shape, torch.float32)
+        ws = _workspace(list_scores_backward_workspace(layout, k), dev, ws)
+        _check(_lib.dsa_list_scores_backward(layout.ref(), _ptr(Q), _ptr(K), _ptr(W), k, _ptr(lists), _ptr(dscores),
+                                             _ptr(dQ), _ptr(dK), _ptr(dW), _ptr(ws), _bytes(ws), _stream(stream)),
+               "dsa_list_scores_backward")
+        _after(ws, "dsa_list_scores_backward", stream)
+    return dQ, dK, dW
 
 
 def launch_count() -> int:

@@ -1,0 +1,316 @@
+// Layer norm of rows and its backward pass.
+//
+// Forward, per row x of d values: mu = mean(x), v = mean((x - mu)^2), r = 1/sqrt(v + eps),
+// y = (x - mu) r w + b.  Backward with xh = (x - mu) r and g = dy w:
+// dx = r (g - mean(g) - xh mean(g xh)), dw = sum over rows of dy xh, db = sum over rows of dy.
+//
+// Both passes are bound by memory: each input is read once and each output written once.  A row is
+// held in the registers of a group of T threads (T * E >= d), so the variance is the two-pass one
+// (centred before it is squared) at no extra read; the sums are fp32.  The weight's gradient is
+// summed in two levels of fixed order: a thread keeps the same columns for every row it handles and
+// adds them up in registers, a CTA joins its row groups through shared memory and writes one
+// partial row, and a second kernel adds the partial rows column by column.
+#pragma once
+
+#include "common.cuh"
+
+namespace dsa {
+
+struct NormArgs {
+    const void* x;
+    int64_t ld_x;
+    const void* dy;     // backward
+    int64_t ld_dy;
+    void* out;          // y, or dx
+    int64_t ld_out;
+    const float* w;     // NULL: ones
+    const float* b;     // NULL: zeros
+    const float* mean_in;
+    const float* rstd_in;
+    float* mean;        // NULL: not written
+    float* rstd;
+    float* part;        // [gridDim.x][2][d] partial sums of the weight's and the bias's gradient
+    int64_t n;
+    int32_t d;
+    float eps;
+};
+
+__device__ __forceinline__ float norm_load(const float* p) { return *p; }
+__device__ __forceinline__ float norm_load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+// VEC consecutive elements as fp32 (VEC 8: 16-byte aligned rows; VEC 1: any).
+template <int VEC>
+__device__ __forceinline__ void norm_load_vec(const float* p, float* v)
+{
+    if constexpr (VEC == 8) {
+        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+        v[0] = *p;
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ void norm_load_vec(const __nv_bfloat16* p, float* v)
+{
+    if constexpr (VEC == 8) {
+        const uint4 a = *reinterpret_cast<const uint4*>(p);
+        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(u[i] << 16);
+            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    } else {
+        v[0] = __bfloat162float(*p);
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ void norm_store_vec(float* p, const float* v)
+{
+    if constexpr (VEC == 8) {
+        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        *p = v[0];
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ void norm_store_vec(__nv_bfloat16* p, const float* v)
+{
+    if constexpr (VEC == 8) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    } else {
+        *p = __float2bfloat16_rn(v[0]);
+    }
+}
+
+// Sum of (a, b) over the T threads of a row group: lanes of one warp, or the whole CTA (T == NT).
+template <int T>
+__device__ __forceinline__ void norm_group_sum(float& a, float& b, float2* red)
+{
+#pragma unroll
+    for (int o = (T < 32 ? T : 32) / 2; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if constexpr (T > 32) {
+        constexpr int NW = T / 32;
+        __syncthreads();   // red is free
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
+        __syncthreads();
+        a = 0.f;
+        b = 0.f;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+            const float2 v = red[i];
+            a += v.x;
+            b += v.y;
+        }
+    }
+}
+
+// NT threads per CTA in groups of T; element e of thread t of a group: column ((e / VEC) * T + t) * VEC + e % VEC.
+template <typename TX, typename TY, int VEC, int T, int NV, int NT>
+__global__ void __launch_bounds__(NT) layer_norm_kernel(const __grid_constant__ NormArgs a)
+{
+    __shared__ float2 red[32];
+    constexpr int G = NT / T;   // rows of a CTA at once
+    const int t = threadIdx.x % T, g = threadIdx.x / T;
+    const float inv_d = 1.f / (float)a.d;
+    for (int64_t row0 = (int64_t)blockIdx.x * G; row0 < a.n; row0 += (int64_t)gridDim.x * G) {
+        const int64_t row = row0 + g;
+        const bool live = row < a.n;
+        const TX* x = static_cast<const TX*>(a.x) + row * a.ld_x;
+        float v[NV][VEC];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * T + t) * VEC;
+            if (live && c < a.d) {
+                norm_load_vec<VEC>(x + c, v[i]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
+            }
+        }
+        float s = 0.f, unused = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s += v[i][e];
+        norm_group_sum<T>(s, unused, red);
+        const float mu = s * inv_d;
+        float q = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const bool in = (i * T + t) * VEC < a.d;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                v[i][e] -= mu;
+                q = in ? fmaf(v[i][e], v[i][e], q) : q;
+            }
+        }
+        unused = 0.f;
+        norm_group_sum<T>(q, unused, red);
+        const float r = 1.f / sqrtf(fmaf(q, inv_d, a.eps));
+        if (!live) continue;
+        if (t == 0) {
+            if (a.mean) a.mean[row] = mu;
+            if (a.rstd) a.rstd[row] = r;
+        }
+        TY* y = static_cast<TY*>(a.out) + row * a.ld_out;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * T + t) * VEC;
+            if (c >= a.d) continue;
+            float w[VEC], b[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) { w[e] = 1.f; b[e] = 0.f; }
+            if (a.w) norm_load_vec<VEC>(a.w + c, w);
+            if (a.b) norm_load_vec<VEC>(a.b + c, b);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) v[i][e] = fmaf(v[i][e] * r, w[e], b[e]);
+            norm_store_vec<VEC>(y + c, v[i]);
+        }
+    }
+}
+
+// TX: the type of x and dx, TY: of dy.  DX: dx is written, DW: the partial sums are.
+template <typename TX, typename TY, int VEC, int T, int NV, int NT>
+__global__ void __launch_bounds__(NT) layer_norm_bwd_kernel(const __grid_constant__ NormArgs a)
+{
+    __shared__ float2 red[32];
+    constexpr int G = NT / T;
+    const int t = threadIdx.x % T, g = threadIdx.x / T;
+    const float inv_d = 1.f / (float)a.d;
+    float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * T + t) * VEC;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            w[i][e] = 1.f;
+            dw[i][e] = db[i][e] = 0.f;
+        }
+        if (a.w && c < a.d) norm_load_vec<VEC>(a.w + c, w[i]);
+    }
+    for (int64_t row0 = (int64_t)blockIdx.x * G; row0 < a.n; row0 += (int64_t)gridDim.x * G) {
+        const int64_t row = row0 + g;
+        const bool live = row < a.n;
+        const TX* x = static_cast<const TX*>(a.x) + row * a.ld_x;
+        const TY* dy = static_cast<const TY*>(a.dy) + row * a.ld_dy;
+        float xh[NV][VEC], gy[NV][VEC];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * T + t) * VEC;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) xh[i][e] = gy[i][e] = 0.f;
+            if (live && c < a.d) {
+                norm_load_vec<VEC>(x + c, xh[i]);
+                norm_load_vec<VEC>(dy + c, gy[i]);
+            }
+        }
+        const float mu = live ? a.mean_in[row] : 0.f, r = live ? a.rstd_in[row] : 0.f;
+        float s1 = 0.f, s2 = 0.f;   // sums of g and of g xh
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const bool in = live && (i * T + t) * VEC < a.d;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                xh[i][e] = in ? (xh[i][e] - mu) * r : 0.f;
+                dw[i][e] = fmaf(gy[i][e], xh[i][e], dw[i][e]);
+                db[i][e] += gy[i][e];
+                gy[i][e] *= w[i][e];
+                s1 += gy[i][e];
+                s2 = fmaf(gy[i][e], xh[i][e], s2);
+            }
+        }
+        norm_group_sum<T>(s1, s2, red);
+        const float m1 = s1 * inv_d, m2 = s2 * inv_d;
+        if (!live || !a.out) continue;
+        TX* dx = static_cast<TX*>(a.out) + row * a.ld_out;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * T + t) * VEC;
+            if (c >= a.d) continue;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) gy[i][e] = r * (gy[i][e] - m1 - xh[i][e] * m2);
+            norm_store_vec<VEC>(dx + c, gy[i]);
+        }
+    }
+    if (!a.part) return;
+    // join the CTA's row groups in order of their number, then one partial row per CTA
+    float* out = a.part + (int64_t)blockIdx.x * 2 * a.d;
+    if constexpr (G == 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * T + t) * VEC;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (c + e < a.d) {
+                    out[c + e] = dw[i][e];
+                    out[a.d + c + e] = db[i][e];
+                }
+        }
+    } else {
+        // groups that share a warp are joined by shuffles, warps through shared memory
+        constexpr int NW = NT / 32, CW = (T < 32 ? T : 32) * NV * VEC;   // columns held by a warp
+        __shared__ float sh[NW][2][CW];
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                float p = dw[i][e], q = db[i][e];
+#pragma unroll
+                for (int o = 16; o >= T; o >>= 1) {
+                    p += __shfl_xor_sync(0xffffffffu, p, o);
+                    q += __shfl_xor_sync(0xffffffffu, q, o);
+                }
+                if ((threadIdx.x & 31) < T) {
+                    sh[threadIdx.x >> 5][0][(i * T + t) * VEC + e] = p;
+                    sh[threadIdx.x >> 5][1][(i * T + t) * VEC + e] = q;
+                }
+            }
+        __syncthreads();
+        for (int c = threadIdx.x; c < 2 * a.d; c += NT) {
+            const int which = c >= a.d, col = c - which * a.d;
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < NW; ++i) s += sh[i][which][col];
+            out[c] = s;
+        }
+    }
+}
+
+// Column sums of part [n_part][2][d]: 32 columns per CTA, 32 threads down each column, joined in order.
+__global__ void __launch_bounds__(1024) layer_norm_dw_kernel(const float* part, int32_t n_part, int32_t d,
+                                                             float* dw, float* db)
+{
+    __shared__ float sh[32][33];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + tx;
+    grid_dep_wait();
+    float s = 0.f;
+    if (c < 2 * d)
+        for (int i = ty; i < n_part; i += 32) s += part[(int64_t)i * 2 * d + c];
+    sh[ty][tx] = s;
+    __syncthreads();
+    if (ty == 0 && c < 2 * d) {
+        float z = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) z += sh[i][tx];
+        float* out = c < d ? dw : db;
+        if (out) out[c < d ? c : c - d] = z;
+    }
+}
+
+}  // namespace dsa

@@ -89,18 +89,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
     }
 }
 
-// One CTA waits, through mbar_wait, on a barrier nothing completes: the wait
-// runs out after limit_ns and records kErrWaitTimeout (the library's
-// failure-reporting self-test).
-__global__ void selftest_wait_kernel(uint32_t* status, uint64_t limit_ns)
-{
-    __shared__ uint64_t bar;
-    if (threadIdx.x != 0) return;
-    mbar_init(&bar, 1);
-    fence_barrier_init();
-    mbar_wait(&bar, 0, status, 0, limit_ns);   // no arrival ever comes
-}
-
 // ------------------------------------------------------------------- TMA
 
 // 2-D tiled bulk tensor load global -> shared, completion counted on `bar`.

@@ -1,0 +1,379 @@
+// libdsaidx C ABI of the operators an indexer is trained with: layer norm, the distillation loss and
+// the indexer's scores at listed keys, with their gradients.  Contract: include/dsa_index.h.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/dsa_index.h"
+#include "distill.cuh"
+#include "host.cuh"
+#include "list_simt.cuh"
+#include "norm.cuh"
+
+using namespace dsa;
+
+namespace {
+
+constexpr int32_t kNormMaxWidth = 16384;
+
+bool type_ok(int32_t t) { return t == DSA_FP32 || t == DSA_BF16; }
+int64_t type_size(int32_t t) { return t == DSA_FP32 ? 4 : 2; }
+
+// A row matrix: rows of d values of the given type, ld values apart.
+dsa_status check_rows(const void* p, int32_t type, int64_t ld, int64_t n, int32_t d)
+{
+    if (!type_ok(type)) return DSA_ERR_UNSUPPORTED;
+    if (n > 0 && !p) return DSA_ERR_INVALID_ARG;
+    if (n > 1 && ld < d) return DSA_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(p) & (type_size(type) - 1)) return DSA_ERR_INVALID_ARG;
+    return DSA_OK;
+}
+
+// Whether every row of the matrix starts on a 16-byte boundary.
+bool rows_aligned(const void* p, int32_t type, int64_t ld, int64_t n)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (n <= 1 || (ld * type_size(type)) % 16 == 0);
+}
+
+// ------------------------------------------------------------- layer norm
+
+// CTAs of the backward pass: as many row groups as fill the GPU (2 CTAs an SM: their partial sums
+// are written and read once more, so more CTAs cost more), fewer for short matrices.
+int32_t norm_bwd_ctas(int64_t n, int32_t groups)
+{
+    return (int32_t)std::max<int64_t>(1, std::min<int64_t>((n + groups - 1) / groups, 2 * 148));
+}
+
+template <typename TX, typename TY, int VEC, int T, int NV, int NT>
+dsa_status norm_launch(const NormArgs& a, bool backward, int32_t* n_part, cudaStream_t st)
+{
+    constexpr int G = NT / T;
+    if (backward) {
+        *n_part = norm_bwd_ctas(a.n, G);
+        DSA_LAUNCH(kProfNorm, st, layer_norm_bwd_kernel<TX, TY, VEC, T, NV, NT><<<*n_part, NT, 0, st>>>(a));
+    } else {
+        const int64_t ctas = std::min<int64_t>((a.n + G - 1) / G, int64_t(148) * (2048 / NT));
+        DSA_LAUNCH(kProfNorm, st, layer_norm_kernel<TX, TY, VEC, T, NV, NT><<<(unsigned)ctas, NT, 0, st>>>(a));
+    }
+    return launched();
+}
+
+// The row group of a width: as few threads as hold the row in at most 16 registers a thread, so a
+// narrow row costs no cross-warp step (128 values of a key: 16 lanes with one 16-byte load each).
+template <typename TX, typename TY>
+dsa_status norm_pick(const NormArgs& a, bool vec, bool bwd, int32_t* np, cudaStream_t st)
+{
+    if (vec) {
+        if (a.d <= 32) return norm_launch<TX, TY, 8, 4, 1, 256>(a, bwd, np, st);
+        if (a.d <= 64) return norm_launch<TX, TY, 8, 8, 1, 256>(a, bwd, np, st);
+        if (a.d <= 128) return norm_launch<TX, TY, 8, 16, 1, 256>(a, bwd, np, st);
+        if (a.d <= 256) return norm_launch<TX, TY, 8, 32, 1, 256>(a, bwd, np, st);
+        if (a.d <= 512) return norm_launch<TX, TY, 8, 32, 2, 256>(a, bwd, np, st);
+        if (a.d <= 1024) return norm_launch<TX, TY, 8, 128, 1, 128>(a, bwd, np, st);
+        if (a.d <= 2048) return norm_launch<TX, TY, 8, 256, 1, 256>(a, bwd, np, st);
+        if (a.d <= 4096) return norm_launch<TX, TY, 8, 256, 2, 256>(a, bwd, np, st);
+        if (a.d <= 8192) return norm_launch<TX, TY, 8, 512, 2, 512>(a, bwd, np, st);
+        return norm_launch<TX, TY, 8, 1024, 2, 1024>(a, bwd, np, st);
+    }
+    if (a.d <= 32) return norm_launch<TX, TY, 1, 32, 1, 256>(a, bwd, np, st);
+    if (a.d <= 128) return norm_launch<TX, TY, 1, 32, 4, 256>(a, bwd, np, st);
+    if (a.d <= 512) return norm_launch<TX, TY, 1, 32, 16, 256>(a, bwd, np, st);
+    if (a.d <= 2048) return norm_launch<TX, TY, 1, 256, 8, 256>(a, bwd, np, st);
+    if (a.d <= 8192) return norm_launch<TX, TY, 1, 512, 16, 512>(a, bwd, np, st);
+    return norm_launch<TX, TY, 1, 1024, 16, 1024>(a, bwd, np, st);
+}
+
+dsa_status norm_dispatch(const NormArgs& a, int32_t tx, int32_t ty, bool vec, bool bwd, int32_t* np, cudaStream_t st)
+{
+    if (tx == DSA_FP32)
+        return ty == DSA_FP32 ? norm_pick<float, float>(a, vec, bwd, np, st)
+                              : norm_pick<float, __nv_bfloat16>(a, vec, bwd, np, st);
+    return ty == DSA_FP32 ? norm_pick<__nv_bfloat16, float>(a, vec, bwd, np, st)
+                          : norm_pick<__nv_bfloat16, __nv_bfloat16>(a, vec, bwd, np, st);
+}
+
+// Partial sums of the weight's and bias's gradients: the most CTAs any row group of the width takes.
+size_t norm_ws_bytes(int64_t n, int32_t d)
+{
+    Carver c{nullptr};
+    c.take<float>(size_t(norm_bwd_ctas(n, 1)) * 2 * d);
+    return c.off;
+}
+
+// ------------------------------------------------------------ distillation
+
+template <typename TT, int VEC, int T, int NV, int NT>
+dsa_status distill_launch(const DistillArgs& a, cudaStream_t st)
+{
+    constexpr int R = NT / T;
+    DSA_LAUNCH(kProfDistill, st, distill_kernel<TT, VEC, T, NV, NT><<<(a.n + R - 1) / R, NT, 0, st>>>(a));
+    return launched();
+}
+
+template <typename TT, int VEC>
+dsa_status distill_pick(const DistillArgs& a, cudaStream_t st)
+{
+    constexpr int U = 4 / VEC;   // registers' worth of a 4-wide load
+    if (a.k <= 128) return distill_launch<TT, VEC, 32, 1 * U, 256>(a, st);
+    if (a.k <= 512) return distill_launch<TT, VEC, 32, 4 * U, 256>(a, st);
+    if (a.k <= 1024) return distill_launch<TT, VEC, 128, 2 * U, 128>(a, st);
+    if (a.k <= 2048) return distill_launch<TT, VEC, 256, 2 * U, 256>(a, st);
+    if (a.k <= 4096) return distill_launch<TT, VEC, 256, 4 * U, 256>(a, st);
+    if (a.k <= 8192) return distill_launch<TT, VEC, 512, 4 * U, 512>(a, st);
+    if (a.k <= kDistillRegCols) return distill_launch<TT, VEC, 1024, 4 * U, 1024>(a, st);
+    DSA_LAUNCH(kProfDistill, st, distill_long_kernel<TT, 1024><<<a.n, 1024, 0, st>>>(a));
+    return launched();
+}
+
+// ----------------------------------------------------- scores at listed keys
+
+struct ListPlan {
+    RowDesc* rows;
+};
+
+size_t list_plan(char* base, const dsa_batch* b, int32_t k, bool backward, ListPlan* p)
+{
+    (void)k;
+    (void)backward;
+    Carver c{base};
+    p->rows = c.take<RowDesc>(std::max(1, b->num_queries));
+    return c.off;
+}
+
+dsa_status list_check(const dsa_batch* b, HostInfo* hi, int32_t k)
+{
+    dsa_status s = check_batch(b, hi);
+    if (s != DSA_OK) return s;
+    return k < 1 || k > kMaxK ? DSA_ERR_UNSUPPORTED : DSA_OK;
+}
+
+ListArgs list_args(const dsa_batch* b, const void* Q, const void* K, const float* W, int32_t k, const int32_t* lists,
+                   const ListPlan& p, void* ws)
+{
+    ListArgs a{};
+    a.rows = p.rows;
+    a.Q = static_cast<const __nv_bfloat16*>(Q);
+    a.K = static_cast<const __nv_bfloat16*>(K);
+    a.W = W;
+    a.lists = lists;
+    a.q_off = b->q_offsets;
+    a.k_off = b->k_offsets;
+    a.status = static_cast<uint32_t*>(ws);
+    a.n_seqs = b->num_seqs;
+    a.n_q = b->num_queries;
+    a.n_k = b->num_keys;
+    a.H = b->num_heads;
+    a.k = k;
+    return a;
+}
+
+dsa_status list_rows(const dsa_batch* b, int32_t k, const int32_t* lists, const ListPlan& p, void* ws, cudaStream_t st)
+{
+    dsa_status s = clear_status(ws, st);
+    if (s != DSA_OK || b->num_queries == 0) return s;
+    DSA_LAUNCH(kProfSetup, st, list_rows_kernel<<<(b->num_queries + 7) / 8, 256, 0, st>>>(
+        lists, k, b->q_offsets, b->k_offsets, b->q_pos, b->num_seqs, b->num_queries, p.rows,
+        static_cast<uint32_t*>(ws)));
+    return launched();
+}
+
+template <int D>
+dsa_status list_scores_d(const ListArgs& a, cudaStream_t st)
+{
+    const size_t smem = size_t(a.H) * D * 4;
+    const dim3 grid(a.n_q, (a.k + kListThreads - 1) / kListThreads);
+    DSA_LAUNCH(kProfListScores, st, list_scores_simt_kernel<D><<<grid, kListThreads, smem, st>>>(a));
+    return launched();
+}
+
+template <int D>
+dsa_status list_backward_d(const ListArgs& a, cudaStream_t st)
+{
+    const size_t smem = (size_t(a.H) * D + kListTile * (D + 1) + kListTile * a.H) * 4;
+    dsa_status s;
+    if (a.n_q > 0 && (a.dQ || a.dW)) {
+        if ((s = set_smem(list_dq_simt_kernel<D>, smem)) != DSA_OK) return s;
+        DSA_LAUNCH(kProfListGrad, st, list_dq_simt_kernel<D><<<a.n_q, kListThreads, smem, st>>>(a));
+        if ((s = launched()) != DSA_OK) return s;
+    }
+    if (a.n_k > 0 && a.dK) {
+        if ((s = set_smem(list_dk_simt_kernel<D>, smem)) != DSA_OK) return s;
+        DSA_LAUNCH(kProfListGrad, st,
+                   list_dk_simt_kernel<D><<<(a.n_k + kListTile - 1) / kListTile, kListThreads, smem, st>>>(a));
+        if ((s = launched()) != DSA_OK) return s;
+    }
+    return DSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+// ------------------------------------------------------------- layer norm
+dsa_status dsa_layer_norm(int64_t n, int32_t d, const void* x, int32_t x_type, int64_t ld_x, const float* weight,
+                          const float* bias, float eps, void* y, int32_t y_type, int64_t ld_y, float* mean,
+                          float* rstd, void* stream)
+{
+    if (n < 0 || d < 1 || !(eps >= 0.f)) return DSA_ERR_INVALID_ARG;
+    if (d > kNormMaxWidth) return DSA_ERR_UNSUPPORTED;
+    dsa_status s;
+    if ((s = check_rows(x, x_type, ld_x, n, d)) != DSA_OK) return s;
+    if ((s = check_rows(y, y_type, ld_y, n, d)) != DSA_OK) return s;
+    if ((reinterpret_cast<uintptr_t>(weight) | reinterpret_cast<uintptr_t>(bias) | reinterpret_cast<uintptr_t>(mean) |
+         reinterpret_cast<uintptr_t>(rstd)) & 3)
+        return DSA_ERR_INVALID_ARG;
+    if (n == 0) return DSA_OK;
+    NormArgs a{};
+    a.x = x; a.ld_x = ld_x; a.out = y; a.ld_out = ld_y; a.w = weight; a.b = bias;
+    a.mean = mean; a.rstd = rstd; a.n = n; a.d = d; a.eps = eps;
+    const bool vec = d % 8 == 0 && rows_aligned(x, x_type, ld_x, n) && rows_aligned(y, y_type, ld_y, n) &&
+                     ((reinterpret_cast<uintptr_t>(weight) | reinterpret_cast<uintptr_t>(bias)) & 15) == 0;
+    int32_t unused = 0;
+    return norm_dispatch(a, x_type, y_type, vec, false, &unused, static_cast<cudaStream_t>(stream));
+}
+
+size_t dsa_layer_norm_backward_workspace(int64_t n, int32_t d)
+{
+    if (n < 0 || d < 1 || d > kNormMaxWidth) return 0;
+    return norm_ws_bytes(n, d);
+}
+
+dsa_status dsa_layer_norm_backward(int64_t n, int32_t d, const void* dy, int32_t dy_type, int64_t ld_dy,
+                                   const void* x, int32_t x_type, int64_t ld_x, const float* weight,
+                                   const float* mean, const float* rstd, void* dx, int64_t ld_dx, float* dweight,
+                                   float* dbias, void* ws, size_t ws_bytes, void* stream)
+{
+    if (n < 0 || d < 1) return DSA_ERR_INVALID_ARG;
+    if (d > kNormMaxWidth) return DSA_ERR_UNSUPPORTED;
+    dsa_status s;
+    if ((s = check_rows(dy, dy_type, ld_dy, n, d)) != DSA_OK) return s;
+    if ((s = check_rows(x, x_type, ld_x, n, d)) != DSA_OK) return s;
+    if (dx && (s = check_rows(dx, x_type, ld_dx, n, d)) != DSA_OK) return s;
+    if (n > 0 && (!mean || !rstd)) return DSA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(weight) | reinterpret_cast<uintptr_t>(mean) | reinterpret_cast<uintptr_t>(rstd) |
+         reinterpret_cast<uintptr_t>(dweight) | reinterpret_cast<uintptr_t>(dbias)) & 3)
+        return DSA_ERR_INVALID_ARG;
+    if ((s = check_ws(ws, ws_bytes, norm_ws_bytes(n, d))) != DSA_OK) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (n == 0) {   // sums over no rows
+        if ((dweight && cudaMemsetAsync(dweight, 0, size_t(d) * 4, st) != cudaSuccess) ||
+            (dbias && cudaMemsetAsync(dbias, 0, size_t(d) * 4, st) != cudaSuccess))
+            return DSA_ERR_CUDA;
+        return DSA_OK;
+    }
+    if (!dx && !dweight && !dbias) return DSA_OK;
+    Carver c{static_cast<char*>(ws)};
+    NormArgs a{};
+    a.x = x; a.ld_x = ld_x; a.dy = dy; a.ld_dy = ld_dy; a.out = dx; a.ld_out = ld_dx; a.w = weight;
+    a.mean_in = mean; a.rstd_in = rstd; a.n = n; a.d = d;
+    a.part = dweight || dbias ? c.take<float>(size_t(norm_bwd_ctas(n, 1)) * 2 * d) : nullptr;
+    const bool vec = d % 8 == 0 && rows_aligned(x, x_type, ld_x, n) && rows_aligned(dy, dy_type, ld_dy, n) &&
+                     (!dx || rows_aligned(dx, x_type, ld_dx, n)) && (reinterpret_cast<uintptr_t>(weight) & 15) == 0;
+    int32_t n_part = 0;
+    if ((s = norm_dispatch(a, x_type, dy_type, vec, true, &n_part, st)) != DSA_OK || !a.part) return s;
+    DSA_LAUNCH(kProfNorm, st, launch_pdl(true, layer_norm_dw_kernel, (2 * d + 31) / 32, 1024, 0, st,
+                                         (const float*)a.part, n_part, d, dweight, dbias));
+    return launched();
+}
+
+// ------------------------------------------------------------ distillation
+dsa_status dsa_distill_topk(int32_t n, int32_t k, const float* scores, int64_t ld_scores, const int32_t* lists,
+                            int64_t ld_lists, const void* teacher, int32_t teacher_type, int64_t ld_teacher,
+                            int32_t teacher_kind, float temperature, const float* grad_loss, float* loss,
+                            float* dscores, int64_t ld_dscores, void* stream)
+{
+    if (n < 0 || k < 1 || !(temperature > 0.f) || !std::isfinite(temperature) ||
+        !std::isfinite(1.f / temperature))
+        return DSA_ERR_INVALID_ARG;
+    if (teacher_kind != DSA_TEACHER_LOGITS && teacher_kind != DSA_TEACHER_WEIGHTS) return DSA_ERR_INVALID_ARG;
+    dsa_status s;
+    if ((s = check_rows(scores, DSA_FP32, ld_scores, n, k)) != DSA_OK) return s;
+    if ((s = check_rows(teacher, teacher_type, ld_teacher, n, k)) != DSA_OK) return s;
+    if (lists && (s = check_rows(lists, DSA_FP32, ld_lists, n, k)) != DSA_OK) return s;
+    if (dscores && (s = check_rows(dscores, DSA_FP32, ld_dscores, n, k)) != DSA_OK) return s;
+    if ((reinterpret_cast<uintptr_t>(grad_loss) | reinterpret_cast<uintptr_t>(loss)) & 3) return DSA_ERR_INVALID_ARG;
+    if (n == 0 || (!loss && !dscores)) return DSA_OK;
+    DistillArgs a{};
+    a.s = scores; a.ld_s = ld_scores; a.list = lists; a.ld_list = ld_lists; a.t = teacher; a.ld_t = ld_teacher;
+    a.g = grad_loss; a.loss = loss; a.ds = dscores; a.ld_ds = ld_dscores; a.n = n; a.k = k;
+    a.weights = teacher_kind == DSA_TEACHER_WEIGHTS ? 1 : 0;
+    a.inv_tau = 1.f / temperature;
+    // four places a load where every row starts on a 16-byte boundary (the teacher's 16-bit rows: 8 bytes)
+    const bool vec = k % 4 == 0 && rows_aligned(scores, DSA_FP32, ld_scores, n) &&
+                     rows_aligned(teacher, teacher_type, teacher_type == DSA_BF16 ? ld_teacher * 2 : ld_teacher, n) &&
+                     (!lists || rows_aligned(lists, DSA_FP32, ld_lists, n)) &&
+                     (!dscores || rows_aligned(dscores, DSA_FP32, ld_dscores, n));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (teacher_type == DSA_FP32) return vec ? distill_pick<float, 4>(a, st) : distill_pick<float, 1>(a, st);
+    return vec ? distill_pick<__nv_bfloat16, 4>(a, st) : distill_pick<__nv_bfloat16, 1>(a, st);
+}
+
+// ----------------------------------------------------- scores at listed keys
+size_t dsa_list_scores_workspace(const dsa_batch* b, int32_t k)
+{
+    HostInfo hi;
+    ListPlan p;
+    return list_check(b, &hi, k) == DSA_OK ? list_plan(nullptr, b, k, false, &p) : 0;
+}
+
+dsa_status dsa_list_scores(const dsa_batch* b, const void* Q, const void* K, const float* W, int32_t k,
+                           const int32_t* lists, float* scores, void* ws, size_t ws_bytes, void* stream)
+{
+    HostInfo hi;
+    dsa_status s = list_check(b, &hi, k);
+    if (s != DSA_OK) return s;
+    if ((s = check_tensors(b, Q, K, W)) != DSA_OK) return s;
+    if (b->num_queries > 0 && (!lists || !scores)) return DSA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(lists) | reinterpret_cast<uintptr_t>(scores)) & 3) return DSA_ERR_INVALID_ARG;
+    ListPlan p;
+    if ((s = check_ws(ws, ws_bytes, list_plan(nullptr, b, k, false, &p))) != DSA_OK) return s;
+    list_plan(static_cast<char*>(ws), b, k, false, &p);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if ((s = list_rows(b, k, lists, p, ws, st)) != DSA_OK || b->num_queries == 0) return s;
+    ListArgs a = list_args(b, Q, K, W, k, lists, p, ws);
+    a.scores = scores;
+    switch (b->head_dim) {
+    case 32: return list_scores_d<32>(a, st);
+    case 64: return list_scores_d<64>(a, st);
+    default: return list_scores_d<128>(a, st);
+    }
+}
+
+size_t dsa_list_scores_backward_workspace(const dsa_batch* b, int32_t k)
+{
+    HostInfo hi;
+    ListPlan p;
+    return list_check(b, &hi, k) == DSA_OK ? list_plan(nullptr, b, k, true, &p) : 0;
+}
+
+dsa_status dsa_list_scores_backward(const dsa_batch* b, const void* Q, const void* K, const float* W, int32_t k,
+                                    const int32_t* lists, const float* dscores, void* dQ, void* dK, float* dW,
+                                    void* ws, size_t ws_bytes, void* stream)
+{
+    HostInfo hi;
+    dsa_status s = list_check(b, &hi, k);
+    if (s != DSA_OK) return s;
+    if ((s = check_tensors(b, Q, K, W)) != DSA_OK) return s;
+    if (b->num_queries > 0 && (!lists || !dscores)) return DSA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(lists) | reinterpret_cast<uintptr_t>(dscores) | reinterpret_cast<uintptr_t>(dW)) & 3)
+        return DSA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(dQ) | reinterpret_cast<uintptr_t>(dK)) & 15) return DSA_ERR_INVALID_ARG;
+    ListPlan p;
+    if ((s = check_ws(ws, ws_bytes, list_plan(nullptr, b, k, true, &p))) != DSA_OK) return s;
+    list_plan(static_cast<char*>(ws), b, k, true, &p);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if ((s = list_rows(b, k, lists, p, ws, st)) != DSA_OK) return s;
+    ListArgs a = list_args(b, Q, K, W, k, lists, p, ws);
+    a.ds = dscores;
+    a.dQ = static_cast<__nv_bfloat16*>(dQ);
+    a.dK = static_cast<__nv_bfloat16*>(dK);
+    a.dW = dW;
+    switch (b->head_dim) {
+    case 32: return list_backward_d<32>(a, st);
+    case 64: return list_backward_d<64>(a, st);
+    default: return list_backward_d<128>(a, st);
+    }
+}
+
+}  // extern "C"
