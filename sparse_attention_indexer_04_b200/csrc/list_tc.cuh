@@ -1,0 +1,504 @@
+// Indexer scores at listed keys and their backward pass on the tensor cores (tcgen05 / TMEM).
+//
+// One query at a time per CTA: its listed keys pass by in tiles of 128, gathered by TMA
+// (four rows per instruction), and
+//   S[128 keys x HP heads] = K_tile . Q^T                 (A = keys, B = heads, both K-major over d)
+//   scores: s[j] = sum_h w_h max(0, S[j,h])               (registers; one key per thread)
+//   backward, with e = ds[j]:
+//     G[j,h] = e w_h where S > 0, else 0, rounded to bf16 into shared memory,
+//     dQ^T[d x HP] += K_tile^T . G                        (both operands MN-major: the gathered tile and G as they lie)
+//     dW_h = sum_j e max(0, S[j,h])                       (fp32 registers, joined once per query)
+// The tile is read once for both products, so a query moves its listed keys from L2 exactly once;
+// that gather (256 bytes per listed pair at d = 128) is what bounds the kernel, not the products.
+// Roles: warps 0, 10, 11 gather; warp 1 issues the MMAs; warps 2..9 are two sets of four that take
+// alternate tiles (one S buffer each), so one set computes while the other's product runs.
+// HP = max(16, H): heads above H have zero rows in the query tile.  Every wait is bounded.
+#pragma once
+
+#include <math_constants.h>
+
+#include "list_simt.cuh"
+#include "ptx.cuh"
+
+namespace dsa {
+
+constexpr int kListTcThreads = 384;
+constexpr int kListTcProducers = 3;
+constexpr uint32_t kErrListAlign = 3;
+
+// Shared-memory matrix descriptor of an MN-major operand: rows of the K dimension are row_bytes
+// (64 or 128) long, swizzled to match, 8-row groups contiguous; blocks of row_bytes along M or N
+// are mn_stride bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_mnmajor(uint32_t addr, uint32_t row_bytes, uint32_t mn_stride)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((mn_stride >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)(((8u * row_bytes) >> 4) & 0x3FFFu) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)(row_bytes == 128 ? 2u : 4u) << 61;
+    return d;
+}
+
+constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;   // operand is MN-major
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v)
+{
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// N (16, 32 or 64) consecutive columns of this thread's TMEM lane; waits for them.
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, float* v)
+{
+    if constexpr (N == 16) {
+        tmem_ld16(taddr, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 32) tmem_ld32(taddr + i, v + i);
+    }
+    tmem_ld_wait();
+    tmem_regs_ready<N>(v);
+}
+
+// tc_wait by a whole warp with one answer (the warp's next steps are warp-wide); false stays false.
+__device__ __forceinline__ bool tc_wait_warp(uint64_t* bar, uint32_t parity, uint32_t* status, uint32_t where,
+                                             volatile int32_t* abort_flag, bool alive)
+{
+    return __all_sync(0xffffffffu, alive && tc_wait(bar, parity, status, where, abort_flag));
+}
+
+__device__ __forceinline__ void named_barrier(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <int D, int HP>
+struct ListShape {
+    static constexpr uint32_t ROWB = D * 2 >= 128 ? 128 : 64;
+    static constexpr int BOXC = ROWB / 2;
+    static constexpr int NBOX = D / BOXC;
+    static constexpr uint32_t KBOX = 128u * ROWB;
+    static constexpr uint32_t KTILE = KBOX * NBOX;
+    static constexpr uint32_t QBOX = (uint32_t)HP * ROWB;
+    static constexpr uint32_t QTILE = QBOX * NBOX;
+    static constexpr uint32_t GTILE = 128u * 128u;   // rows of 128 bytes, the first HP heads used
+    static constexpr uint32_t W_BYTES = 2u * 2u * HP * 4;         // [set][parity][head]
+    static constexpr uint32_t DW_BYTES = 2u * 8u * HP * 4;        // [parity][warp][head]
+    static constexpr uint32_t BAR_BYTES = 512;
+    static constexpr uint32_t align1k(uint32_t x) { return (x + 1023u) & ~1023u; }
+    // key stages, query tiles, G tiles, then the small arrays.  An operand tile narrower than the
+    // MMA's 128 rows (d < 128) reads past itself into what follows: rows nobody looks at.
+    static constexpr uint32_t q_off(int stages) { return stages * KTILE; }
+    static constexpr uint32_t g_off(int stages) { return q_off(stages) + align1k(2 * QTILE); }
+    static constexpr uint32_t w_off(int stages) { return g_off(stages) + 2 * GTILE; }
+    static constexpr uint32_t bytes(int stages) { return w_off(stages) + W_BYTES + DW_BYTES + BAR_BYTES; }
+};
+
+struct ListTcArgs {
+    ListArgs l;
+    int32_t n_stages;
+};
+
+// Sums 32 / 64 per-lane values over the warp: lane i ends with the sums of values i (and i + 32).
+// A butterfly that halves the number of values at each step: N values cost about N + N/2 shuffles.
+template <int N>
+__device__ __forceinline__ void warp_transpose_sum(float* v, int lane)
+{
+    if constexpr (N == 64) {
+        // two interleaved halves of 32
+        warp_transpose_sum<32>(v, lane);
+        warp_transpose_sum<32>(v + 32, lane);
+    } else {
+#pragma unroll
+        for (int o = N / 2; o > 0; o >>= 1) {
+            const bool up = lane & o;
+#pragma unroll
+            for (int i = 0; i < o; ++i) {
+                const float send = up ? v[i] : v[i + o];
+                const float keep = up ? v[i + o] : v[i];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+        }
+        if constexpr (N == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
+    }
+}
+
+template <int D, int HP, bool BWD>
+__global__ void __launch_bounds__(kListTcThreads, 1)
+    list_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmKg,
+                   const __grid_constant__ ListTcArgs a)
+{
+    using SH = ListShape<D, HP>;
+    constexpr int NP = kListTcProducers;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint32_t* status = a.l.status;
+    if (smem_u32(smem) & 1023u) {
+        if (threadIdx.x == 0) record_error(status, kErrListAlign, blockIdx.x);
+        return;
+    }
+    const int n_stages = a.n_stages;
+    uint8_t* sK = smem;
+    uint8_t* sQ = smem + SH::q_off(n_stages);
+    uint8_t* sG = smem + SH::g_off(n_stages);
+    float* sW = reinterpret_cast<float*>(smem + SH::w_off(n_stages));
+    float* sDW = sW + SH::W_BYTES / 4;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + SH::w_off(n_stages) + SH::W_BYTES + SH::DW_BYTES);
+    uint64_t* kempty = full + NP * n_stages;   // the tile's products have read it
+    uint64_t* qfull = kempty + n_stages;       // [2] the query tile has landed
+    uint64_t* qempty = qfull + 2;              // [2] its last product has read it
+    uint64_t* sfull = qempty + 2;              // [2] S is complete
+    uint64_t* sfree = sfull + 2;               // [2] S has been read
+    uint64_t* gfull = sfree + 2;               // [2] G is written
+    uint64_t* gfree = gfull + 2;               // [2] G has been read
+    uint64_t* dqfull = gfree + 2;              // [2] dQ of a query is complete
+    uint64_t* dqfree = dqfull + 2;             // [2] dQ has been read
+    uint64_t* drain = dqfree + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NP * n_stages; ++i) mbar_init(&full[i], 1);
+        for (int i = 0; i < n_stages; ++i) mbar_init(&kempty[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&qfull[i], 1);
+            mbar_init(&qempty[i], 1);
+            mbar_init(&sfull[i], 1);
+            mbar_init(&sfree[i], 128);
+            mbar_init(&gfull[i], 128);
+            mbar_init(&gfree[i], 1);
+            mbar_init(&dqfull[i], 1);
+            mbar_init(&dqfree[i], 256);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&tmQ);
+        prefetch_tensormap(&tmKg);
+    }
+    // heads above H: zero rows that no load overwrites
+    for (uint32_t i = threadIdx.x; i < SH::align1k(2 * SH::QTILE) / 4; i += kListTcThreads)
+        reinterpret_cast<uint32_t*>(sQ)[i] = 0u;
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    if (warp == 1) tmem_alloc(tmem_slot, 256);
+    grid_dep_wait();   // the rows come from the set-up kernel
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tS = tmem, tDQ = tmem + 128;
+    const int n_q = a.l.n_q, H = a.l.H, k = a.l.k, step = gridDim.x;
+    const RowDesc none{0, 0, 0, 0};
+
+    if (warp == 0 || warp >= 10) {
+        // ------------------------------------------------------ producers
+        const int pw = warp == 0 ? 0 : warp - 9;
+        constexpr int kItems = 32 * SH::NBOX;
+        const int w = lane * NP + pw;
+        const bool has_item = w < kItems;
+        const int rg = w % 32, ibox = w / 32;
+        const uint32_t my_bytes = (uint32_t)((kItems - pw + NP - 1) / NP) * 4 * SH::ROWB;
+        uint64_t* my_full = full + pw * n_stages;
+        const uint64_t keep_keys = l2_policy_evict_last();
+        int stage = 0, it = 0;
+        uint32_t phase = 0;
+        int issued = 0;
+        int q_issued = 0;
+        bool alive = true;
+        RowDesc nx = (int)blockIdx.x < n_q ? a.l.rows[blockIdx.x] : none;
+        for (int t = blockIdx.x; t < n_q && alive; t += step) {
+            const RowDesc r = nx;
+            if (t + step < n_q) nx = a.l.rows[t + step];
+            const int nt = (r.ncols + 127) >> 7;
+            if (nt == 0) continue;
+            const int qb = it & 1;
+            if (pw == 0) {
+                int ok = 1;
+                if (lane == 0) {
+                    ok = tc_wait(&qempty[qb], ((it >> 1) & 1) ^ 1u, status, 21, abort_flag) ? 1 : 0;
+                    if (ok) {
+                        mbar_arrive_expect_tx(&qfull[qb], (uint32_t)H * D * 2);
+                        for (int bx = 0; bx < SH::NBOX; ++bx)
+                            tma_load_2d(sQ + qb * SH::QTILE + bx * SH::QBOX, &tmQ, bx * SH::BOXC, t * H, &qfull[qb]);
+                    }
+                }
+                if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+                ++q_issued;
+            }
+            ++it;
+            const int32_t* l = a.l.lists + (int64_t)t * k;
+            const int krow0 = a.l.k_off[r.seq];
+            const bool list4 = (reinterpret_cast<uintptr_t>(l) & 15) == 0;
+            auto tile_rows = [&](int i, int (&y)[4]) {
+                const int c0 = i * 128 + 4 * rg;
+                if (c0 + 3 < r.ncols && list4) {
+                    const int4 v = __ldg(reinterpret_cast<const int4*>(l + c0));
+                    y[0] = krow0 + v.x; y[1] = krow0 + v.y; y[2] = krow0 + v.z; y[3] = krow0 + v.w;
+                } else {   // places behind the last take its key again
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = krow0 + __ldg(l + min(c0 + e, r.ncols - 1));
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!DSA_CHECK(y[e] >= 0 && y[e] < a.l.n_k, status, 113)) y[e] = 0;
+            };
+            int ynext[4] = {0, 0, 0, 0};
+            if (has_item) tile_rows(0, ynext);
+            for (int i = 0; i < nt; ++i) {
+                int ok = 1;
+                if (lane == 0) ok = tc_wait(&kempty[stage], phase ^ 1u, status, 22, abort_flag) ? 1 : 0;
+                if (!__shfl_sync(0xffffffffu, ok, 0)) { alive = false; break; }
+                if (lane == 0) mbar_arrive_expect_tx(&my_full[stage], my_bytes);
+                __syncwarp();
+                if (has_item) {
+                    const int y[4] = {ynext[0], ynext[1], ynext[2], ynext[3]};
+                    tma_gather4_2d_hint(sK + stage * SH::KTILE + ibox * SH::KBOX + 4 * rg * SH::ROWB, &tmKg,
+                                        ibox * SH::BOXC, y[0], y[1], y[2], y[3], &my_full[stage], keep_keys);
+                    if (i + 1 < nt) tile_rows(i + 1, ynext);
+                }
+                ++issued;
+                if (++stage == n_stages) { stage = 0; phase ^= 1u; }
+            }
+        }
+        if (lane == 0 && *abort_flag) {   // every copy this warp started must have landed
+            for (int back = 1; back <= 2 && back <= q_issued; ++back) {
+                const int i = q_issued - back;
+                mbar_wait(&qfull[i & 1], (uint32_t)((i >> 1) & 1), status, 23);
+            }
+            for (int back = 1; back <= n_stages && back <= issued; ++back) {
+                const int i = issued - back;
+                mbar_wait(&my_full[i % n_stages], (uint32_t)((i / n_stages) & 1), status, 24);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // -------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            const uint32_t idS = idesc_bf16_f32(128, HP);
+            const uint32_t idQ = idesc_bf16_f32(128, HP) | kIdescAMn | kIdescBMn;
+            int stage = 0;
+            uint32_t phase = 0;
+            int n = 0, it = 0;     // tiles and non-empty queries so far
+            // the product of the tile before, issued after the next tile's S so that the two overlap
+            bool pend = false, pend_first = false, pend_last = false;
+            int pend_stage = 0, pend_it = 0, pend_n = 0;
+            bool alive = true;
+            auto flush = [&]() {
+                if (!pend || !alive) return;
+                pend = false;
+                const int b = pend_n & 1, qb = pend_it & 1;
+                if (!tc_wait(&gfull[b], (pend_n >> 1) & 1, status, 25, abort_flag)) { alive = false; return; }
+                if (pend_first && !tc_wait(&dqfree[qb], ((pend_it >> 1) & 1) ^ 1u, status, 26, abort_flag)) {
+                    alive = false;
+                    return;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {   // 16 keys each
+                    const uint64_t ad = smem_desc_mnmajor(
+                        smem_u32(sK + pend_stage * SH::KTILE) + kk * 16 * SH::ROWB, SH::ROWB, SH::KBOX);
+                    const uint64_t bd = smem_desc_mnmajor(smem_u32(sG + b * SH::GTILE) + kk * 16 * 128, 128, 0);
+                    tc_mma(tDQ + qb * 64, ad, bd, idQ, kk > 0 || !pend_first ? 1u : 0u);
+                }
+                tc_commit(&kempty[pend_stage]);
+                tc_commit(&gfree[b]);
+                if (pend_last) tc_commit(&dqfull[qb]);
+            };
+            RowDesc nx = (int)blockIdx.x < n_q ? a.l.rows[blockIdx.x] : none;
+            for (int t = blockIdx.x; t < n_q && alive; t += step) {
+                const RowDesc r = nx;
+                if (t + step < n_q) nx = a.l.rows[t + step];
+                const int nt = (r.ncols + 127) >> 7;
+                if (nt == 0) continue;
+                const int qb = it & 1;
+                if (!tc_wait(&qfull[qb], (it >> 1) & 1, status, 27, abort_flag)) break;
+                for (int i = 0; i < nt && alive; ++i, ++n) {
+                    const int b = n & 1;
+                    for (int p = 0; p < NP && alive; ++p)
+                        alive = tc_wait(&full[p * n_stages + stage], phase, status, 28, abort_flag);
+                    if (!alive) break;
+                    if (!tc_wait(&sfree[b], ((n >> 1) & 1) ^ 1u, status, 29, abort_flag)) { alive = false; break; }
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const int bx = kk / (SH::BOXC / 16);
+                        const uint32_t ko = (kk % (SH::BOXC / 16)) * 32;
+                        const uint64_t ad =
+                            smem_desc_kmajor(smem_u32(sK + stage * SH::KTILE + bx * SH::KBOX) + ko, SH::ROWB);
+                        const uint64_t bd =
+                            smem_desc_kmajor(smem_u32(sQ + qb * SH::QTILE + bx * SH::QBOX) + ko, SH::ROWB);
+                        tc_mma(tS + b * 64, ad, bd, idS, kk > 0 ? 1u : 0u);
+                    }
+                    tc_commit(&sfull[b]);
+                    if (i == nt - 1) tc_commit(&qempty[qb]);
+                    if constexpr (BWD) {
+                        flush();
+                        pend = true;
+                        pend_first = i == 0;
+                        pend_last = i == nt - 1;
+                        pend_stage = stage;
+                        pend_it = it;
+                        pend_n = n;
+                    } else {
+                        tc_commit(&kempty[stage]);
+                    }
+                    if (++stage == n_stages) { stage = 0; phase ^= 1u; }
+                }
+                ++it;
+            }
+            if constexpr (BWD) flush();
+            tc_commit(drain);   // every MMA issued has completed before TMEM is released
+            mbar_wait(drain, 0, status, 30);
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------- epilogue
+        // Named barriers are met by all threads of a set whatever an abort makes of the waits, so the
+        // loops run to their end with `alive` false instead of leaving.
+        const int quarter = warp & 3;           // TMEM lanes this warp may read
+        const int set = (warp - 2) >> 2;
+        const int lrow = quarter * 32 + lane;   // key of the tile
+        const int st = threadIdx.x - 64 - set * 128;   // thread of the set
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        int n = 0, it = 0, all = 0;
+        bool alive = true;
+        RowDesc nx = (int)blockIdx.x < n_q ? a.l.rows[blockIdx.x] : none;
+        float wnext = st < H && (int)blockIdx.x < n_q ? a.l.W[(int64_t)blockIdx.x * H + st] : 0.f;
+        for (int t = blockIdx.x; t < n_q; t += step, ++all) {
+            const RowDesc r = nx;
+            float* w = sW + (set * 2 + (all & 1)) * HP;
+            if (st < HP) w[st] = wnext;
+            if (t + step < n_q) {
+                nx = a.l.rows[t + step];
+                wnext = st < H ? a.l.W[(int64_t)(t + step) * H + st] : 0.f;
+            }
+            named_barrier(1 + set, 128);
+            const int nt = (r.ncols + 127) >> 7;
+            [[maybe_unused]] float dw[HP];
+            if constexpr (BWD) {
+#pragma unroll
+                for (int h = 0; h < HP; ++h) dw[h] = 0.f;
+            }
+            int i = (n & 1) == set ? 0 : 1;   // the set's first tile
+            float e = 0.f;
+            if (BWD && i * 128 + lrow < r.ncols) e = a.l.ds[(int64_t)t * k + i * 128 + lrow];
+            for (; i < nt; i += 2) {
+                const int g = n + i;   // the CTA's tile number
+                alive = tc_wait_warp(&sfull[set], (g >> 1) & 1, status, 31, abort_flag, alive);
+                if (!alive) continue;
+                tc_fence_after();
+                float v[HP];
+                tmem_load<HP>(tS + set * 64 + lanes, v);
+                tc_fence_before();
+                mbar_arrive(&sfree[set]);
+                const int j = i * 128 + lrow;
+                if constexpr (!BWD) {
+                    uint64_t acc = 0;   // even heads and odd heads
+#pragma unroll
+                    for (int h = 0; h < HP; h += 4) {
+                        const float4 w4 = *reinterpret_cast<const float4*>(w + h);
+                        acc = fma_f32x2(pack_f32x2(w4.x, w4.y), pack_f32x2(fmaxf(v[h], 0.f), fmaxf(v[h + 1], 0.f)), acc);
+                        acc = fma_f32x2(pack_f32x2(w4.z, w4.w), pack_f32x2(fmaxf(v[h + 2], 0.f), fmaxf(v[h + 3], 0.f)), acc);
+                    }
+                    float s0, s1;
+                    unpack_f32x2(acc, s0, s1);
+                    if (j < k) a.l.scores[(int64_t)t * k + j] = j < r.ncols ? (s0 + s1) + 0.f : -CUDART_INF_F;
+                } else {
+                    const float ej = j < r.ncols ? e : 0.f;
+                    if (j + 256 < r.ncols) e = a.l.ds[(int64_t)t * k + j + 256];
+                    // a place behind the list's end repeats the last key: its products count for nothing (e = 0)
+                    alive = tc_wait_warp(&gfree[set], ((g >> 1) & 1) ^ 1u, status, 32, abort_flag, alive);
+                    if (!alive) continue;
+                    uint8_t* grow = sG + set * SH::GTILE + lrow * 128;
+#pragma unroll
+                    for (int h0 = 0; h0 < HP; h0 += 8) {
+                        uint32_t p[4];
+#pragma unroll
+                        for (int h = 0; h < 8; h += 4) {
+                            const float4 w4 = *reinterpret_cast<const float4*>(w + h0 + h);
+                            const float wv[4] = {w4.x, w4.y, w4.z, w4.w};
+                            float gv[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const float s = v[h0 + h + x];
+                                dw[h0 + h + x] = fmaf(ej, fmaxf(s, 0.f), dw[h0 + h + x]);
+                                gv[x] = s > 0.f ? ej * wv[x] : 0.f;
+                            }
+                            p[h / 2] = pack_bf16x2(gv[0], gv[1]);
+                            p[h / 2 + 1] = pack_bf16x2(gv[2], gv[3]);
+                        }
+                        *reinterpret_cast<uint4*>(grow + (((h0 / 8) ^ (lrow & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    mbar_arrive(&gfull[set]);
+                }
+            }
+            n += nt;
+            if constexpr (!BWD) {
+                // places behind the last tile (set 0's threads, which may still be a tile ahead or behind)
+                if (set == 0)
+                    for (int j = nt * 128 + st; j < k; j += 128) a.l.scores[(int64_t)t * k + j] = -CUDART_INF_F;
+            } else {
+                warp_transpose_sum<HP>(dw, lane);
+                float* part = sDW + ((all & 1) * 8 + (warp - 2)) * HP;
+                if (lane < HP) part[lane] = dw[0];
+                if (HP == 64) part[lane + 32] = dw[32];
+                named_barrier(3, 256);
+                if (a.l.dW && set == 0 && st < H) {
+                    float s = 0.f;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) s += sDW[((all & 1) * 8 + x) * HP + st];
+                    a.l.dW[(int64_t)t * H + st] = s;
+                }
+                constexpr int NC = HP == 16 ? 16 : HP / 2;   // columns (heads) a set writes
+                const int c0 = HP == 16 ? 0 : set * NC;
+                if (nt > 0) {
+                    const int qb = it & 1;
+                    alive = tc_wait_warp(&dqfull[qb], (it >> 1) & 1, status, 33, abort_flag, alive);
+                    if (alive) {
+                        tc_fence_after();
+                        float v[NC];
+                        if (HP > 16 || set == 0) tmem_load<NC>(tDQ + qb * 64 + c0 + lanes, v);
+                        tc_fence_before();
+                        mbar_arrive(&dqfree[qb]);
+                        if (a.l.dQ && lrow < D && (HP > 16 || set == 0)) {
+                            __nv_bfloat16* out = a.l.dQ + ((int64_t)t * H + c0) * D + lrow;
+#pragma unroll
+                            for (int c = 0; c < NC; ++c)
+                                if (c0 + c < H) out[c * D] = __float2bfloat16_rn(v[c]);
+                        }
+                    }
+                } else if (a.l.dQ) {   // nothing listed: zero gradients
+                    for (int o = threadIdx.x - 64; o < H * D; o += 256)
+                        a.l.dQ[(int64_t)t * H * D + o] = __float2bfloat16_rn(0.f);
+                }
+            }
+            if (nt > 0) ++it;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 256);
+    }
+}
+
+}  // namespace dsa

@@ -101,24 +101,6 @@ __device__ __forceinline__ uint32_t dynamic_smem_size()
     return x;
 }
 
-__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, uint32_t* status, uint32_t where,
-                                        volatile int32_t* abort_flag)
-{
-    if (mbar_test(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
-#pragma unroll 1
-        for (int i = 0; i < 256; ++i)
-            if (mbar_test(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (global_timer_ns() - t0 > kWaitLimitNs) {
-            record_error(status, kErrWaitTimeout, where);
-            *abort_flag = 1;
-            return false;
-        }
-    }
-}
-
 // MODE kTcTiles: contiguous key tiles; kTcGather: the unit's key tiles are gathered through the
 // column map (a.gather == 1); kTcBlocks: contiguous tiles at computed rows, the three planes of
 // fp32 keys (a.planes) or whole 128-key tiles of a block map (a.block_tiles).  The cases are

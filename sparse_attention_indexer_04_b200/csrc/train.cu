@@ -9,6 +9,7 @@
 #include "distill.cuh"
 #include "host.cuh"
 #include "list_simt.cuh"
+#include "list_tc.cuh"
 #include "norm.cuh"
 
 using namespace dsa;
@@ -178,13 +179,36 @@ dsa_status list_rows(const dsa_batch* b, int32_t k, const int32_t* lists, const 
     return launched();
 }
 
+constexpr int kSmemMax = 232448;   // dynamic shared memory of one CTA
+
+template <int D, int HP, bool BWD>
+dsa_status list_tc_launch(const ListArgs& l, cudaStream_t st)
+{
+    using SH = ListShape<D, HP>;
+    CUtensorMap mq, mk;
+    if (!make_tile_map(&mq, l.Q, int64_t(l.n_q) * l.H, D, l.H) || !make_tile_map(&mk, l.n_k > 0 ? l.K : l.Q, l.n_k > 0 ? l.n_k : l.n_q, D, 1))   // (no keys: never read)
+        return DSA_ERR_CUDA;
+    ListTcArgs a{l, std::min(8, int((kSmemMax - SH::bytes(0)) / SH::KTILE))};
+    const int smem = std::max<int>(SH::bytes(a.n_stages), 120 * 1024);   // one CTA an SM
+    dsa_status s = set_smem(list_tc_kernel<D, HP, BWD>, smem);
+    if (s != DSA_OK) return s;
+    DSA_LAUNCH(BWD ? kProfListGrad : kProfListScores, st,
+               launch_pdl(true, list_tc_kernel<D, HP, BWD>, std::min(l.n_q, 148), kListTcThreads, smem, st, mq, mk, a));
+    return launched();
+}
+
+template <int D, bool BWD>
+dsa_status list_tc(const ListArgs& a, cudaStream_t st)
+{
+    if (a.H <= 16) return list_tc_launch<D, 16, BWD>(a, st);
+    if (a.H <= 32) return list_tc_launch<D, 32, BWD>(a, st);
+    return list_tc_launch<D, 64, BWD>(a, st);
+}
+
 template <int D>
 dsa_status list_scores_d(const ListArgs& a, cudaStream_t st)
 {
-    const size_t smem = size_t(a.H) * D * 4;
-    const dim3 grid(a.n_q, (a.k + kListThreads - 1) / kListThreads);
-    DSA_LAUNCH(kProfListScores, st, list_scores_simt_kernel<D><<<grid, kListThreads, smem, st>>>(a));
-    return launched();
+    return list_tc<D, false>(a, st);
 }
 
 template <int D>
@@ -193,9 +217,7 @@ dsa_status list_backward_d(const ListArgs& a, cudaStream_t st)
     const size_t smem = (size_t(a.H) * D + kListTile * (D + 1) + kListTile * a.H) * 4;
     dsa_status s;
     if (a.n_q > 0 && (a.dQ || a.dW)) {
-        if ((s = set_smem(list_dq_simt_kernel<D>, smem)) != DSA_OK) return s;
-        DSA_LAUNCH(kProfListGrad, st, list_dq_simt_kernel<D><<<a.n_q, kListThreads, smem, st>>>(a));
-        if ((s = launched()) != DSA_OK) return s;
+        if ((s = list_tc<D, true>(a, st)) != DSA_OK) return s;
     }
     if (a.n_k > 0 && a.dK) {
         if ((s = set_smem(list_dk_simt_kernel<D>, smem)) != DSA_OK) return s;
