@@ -142,10 +142,10 @@ inline bool latency_bound(int64_t ctas) { return ctas <= 2 * 148; }
 // Kernel kinds timed by the optional profiler (dsa_profile_*).
 enum ProfKind : int32_t {
     kProfSetup = 0, kProfScoreSimt, kProfSelect, kProfPool, kProfProxy, kProfScoreTc, kProfFill, kProfNorm,
-    kProfDistill, kProfListScores, kProfListGrad, kProfKinds
+    kProfDistill, kProfListScores, kProfListDq, kProfListDk, kProfKinds
 };
 inline const char* const kProfNames[kProfKinds] = {"setup", "score_simt", "select_topk", "hisa_pool", "pivot_proxy",
-                                            "score_tc", "fill", "layer_norm", "distill", "list_scores", "list_grad"};
+                                            "score_tc", "fill", "layer_norm", "distill", "list_scores", "list_dq", "list_dk"};
 
 struct ProfRec {
     int32_t kind;

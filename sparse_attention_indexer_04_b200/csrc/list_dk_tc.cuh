@@ -1,0 +1,409 @@
+// dK of the scores at listed keys on the tensor cores: dK[s] = sum over (t, h) of G[t,s,h] q[t,h],
+// G = ds w where q . k > 0 and t lists s, else 0.
+//
+// The sum runs over queries, so the keys stay: a CTA owns 256 consecutive keys of a sequence (two
+// tiles of 128, resident in shared memory, their dK accumulators in TMEM for the CTA's whole life)
+// and passes over the queries that list any of them, NQ = up to 64 / H at a time:
+//   S[128 keys x ROWS] = K_tile . Q^T      (ROWS = NQ * H query-head rows)
+//   G = S > 0 ? ds w : 0                    (bf16, shared memory; ds scattered from the list's places)
+//   dK_tile += G . Q                        (A = G K-major, B = Q MN-major as it lies)
+// No atomics and no scatter of rows: each (key tile, query) product is dense, keys that the query does
+// not list have G = 0.  That does up to 1 / density of the needed work, but the alternative, a
+// 512-byte fp32 row added to memory per listed pair, costs more until lists cover less than about
+// a tenth of the prefix.  The queries of a sequence are dealt to `parts` CTAs per key block when there
+// are few key blocks; their fp32 partial sums are added in order by a second kernel.
+// Roles: warps 0..3 load (one stage each: query rows, weights and the block's ds), warp 4 issues
+// the MMAs, warps 5..12 are two sets of four, one per key tile.  Every wait is bounded.
+#pragma once
+
+#include "list_tc.cuh"
+
+namespace dsa {
+
+constexpr int kDkThreads = 416;
+constexpr int kDkKeys = 256;
+constexpr int kDkMaxList = 8192;   // queries of one CTA at most
+
+// Per query and block of kDkKeys keys, the first list place at or behind the block's start:
+// edge[block][n_q], for blocks 0 .. max_blocks (the last row: the usable length).  One warp per query.
+__global__ void list_edges_kernel(const int32_t* lists, int32_t k, const RowDesc* rows, int32_t n_q, int32_t n_blocks,
+                                  uint16_t* edge)
+{
+    const int t = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (t >= n_q) return;
+    const int n = rows[t].ncols;
+    const int32_t* l = lists + (int64_t)t * k;
+    for (int i = lane; i <= n; i += 32) {
+        const int lo = i > 0 ? l[i - 1] / kDkKeys + 1 : 0;       // blocks that start behind place i - 1
+        const int hi = i < n ? l[i] / kDkKeys : n_blocks;        // and at or before place i
+        for (int b = lo; b <= hi; ++b) edge[(int64_t)b * n_q + t] = (uint16_t)i;
+    }
+}
+
+template <int D, int H>
+struct DkShape {
+    static constexpr int NQ = H >= 8 ? 64 / H : H >= 2 ? 8 : 16;   // queries of a block
+    static constexpr int ROWS = NQ * H;                            // 16, 32 or 64
+    static constexpr uint32_t ROWB = D * 2 >= 128 ? 128 : 64;
+    static constexpr int BOXC = ROWB / 2;
+    static constexpr int NBOX = D / BOXC;
+    static constexpr uint32_t KBOX = 128u * ROWB;
+    static constexpr uint32_t KTILE = KBOX * NBOX;
+    static constexpr uint32_t QBOX = (uint32_t)ROWS * ROWB;
+    static constexpr uint32_t QTILE = QBOX * NBOX;
+    static constexpr uint32_t GTILE = 128u * 128u;
+    static constexpr int NS = NQ >= 8 ? 3 : 4;                     // stages of queries
+    static constexpr uint32_t E_BYTES = (uint32_t)NQ * kDkKeys * 4;
+    static constexpr uint32_t q_off = 2 * KTILE;
+    static constexpr uint32_t g_off = q_off + NS * QTILE;          // [tile][parity]
+    static constexpr uint32_t e_off = g_off + 4 * GTILE;
+    static constexpr uint32_t w_off = e_off + NS * E_BYTES;
+    static constexpr uint32_t list_off = w_off + NS * 64 * 4;
+    static constexpr uint32_t bar_off = list_off + kDkMaxList * 2;
+    static constexpr uint32_t bytes = bar_off + 512;
+    static_assert(NS <= 4 && ROWS % (32 / (D / 8)) == 0);
+    static_assert(g_off % 1024 == 0 && q_off % 1024 == 0 && bytes <= 232448, "shared memory of the dK kernel");
+};
+
+struct DkArgs {
+    ListArgs l;
+    const uint16_t* edge;   // [max blocks + 1][n_q]
+    float* part;            // [parts][n_k][D] (parts > 1)
+    int32_t parts;
+};
+
+// First unit of sequence b: at least as many units as key blocks, without a table.
+__device__ __forceinline__ int dk_unit_base(const int32_t* k_off, int b) { return k_off[b] / kDkKeys + b; }
+
+template <int D, int H>
+__global__ void __launch_bounds__(kDkThreads, 1)
+    list_dk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ DkArgs a)
+{
+    using SH = DkShape<D, H>;
+    constexpr int NQ = SH::NQ, ROWS = SH::ROWS, NS = SH::NS;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint32_t* status = a.l.status;
+    if (smem_u32(smem) & 1023u) {
+        if (threadIdx.x == 0) record_error(status, kErrListAlign, blockIdx.x);
+        return;
+    }
+    const int unit = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
+    // the unit's sequence and key block
+    int seq = 0;
+    {
+        int hi = a.l.n_seqs - 1;
+        while (seq < hi) {
+            const int mid = (seq + hi + 1) >> 1;
+            if (dk_unit_base(a.l.k_off, mid) <= unit) seq = mid; else hi = mid - 1;
+        }
+    }
+    const int blk = unit - dk_unit_base(a.l.k_off, seq);
+    const int kb = a.l.k_off[seq], L = a.l.k_off[seq + 1] - kb;
+    const int s0 = blk * kDkKeys;
+    if (s0 >= L) return;   // a unit without keys
+    const int q0 = a.l.q_off[seq], nq = a.l.q_off[seq + 1] - q0;
+
+    uint8_t* sK = smem;
+    uint8_t* sQ = smem + SH::q_off;
+    uint8_t* sG = smem + SH::g_off;
+    float* sE = reinterpret_cast<float*>(smem + SH::e_off);
+    float* sW = reinterpret_cast<float*>(smem + SH::w_off);
+    uint16_t* sList = reinterpret_cast<uint16_t*>(smem + SH::list_off);
+    uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + SH::bar_off);
+    uint64_t* qfull = kfull + 1;          // [NS] query rows have landed
+    uint64_t* qfree = qfull + NS;         // [NS] both products have read them
+    uint64_t* efull = qfree + NS;         // [NS] ds and weights are written
+    uint64_t* efree = efull + NS;         // [NS] and read
+    uint64_t* sfull = efree + NS;         // [tile][parity]
+    uint64_t* sfree = sfull + 4;
+    uint64_t* gfull = sfree + 4;
+    uint64_t* gfree = gfull + 4;
+    uint64_t* dkfull = gfree + 4;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dkfull + 1);
+    volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
+    int32_t* sCount = reinterpret_cast<int32_t*>(tmem_slot + 2);   // [14] per-warp counts, then the total
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        mbar_init(kfull, 1);
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&qfull[i], 32);
+            mbar_init(&qfree[i], 1);
+            mbar_init(&efull[i], 32);
+            mbar_init(&efree[i], 256);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&sfull[i], 1);
+            mbar_init(&sfree[i], 128);
+            mbar_init(&gfull[i], 128);
+            mbar_init(&gfree[i], 1);
+        }
+        mbar_init(dkfull, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&tmK);
+    }
+    if (warp == 4) tmem_alloc(tmem_slot, 512);
+
+    // the part's queries that list a key of the block, in order (query part + ordinal * parts)
+    const uint16_t* e0 = a.edge + (int64_t)blk * a.l.n_q + q0;
+    const uint16_t* e1 = e0 + a.l.n_q;
+    const int n_cand = nq > part ? (nq - part + a.parts - 1) / a.parts : 0;
+    int m = 0;
+    for (int c0 = 0; c0 < n_cand; c0 += kDkThreads) {
+        const int c = c0 + threadIdx.x, t = part + c * a.parts;
+        const bool on = c < n_cand && e1[t] > e0[t];
+        const uint32_t vote = __ballot_sync(0xffffffffu, on);
+        if (lane == 0) sCount[warp] = __popc(vote);
+        __syncthreads();
+        int before = m, total = 0;
+        for (int w = 0; w < kDkThreads / 32; ++w) {
+            if (w < warp) before += sCount[w];
+            total += sCount[w];
+        }
+        if (on && DSA_CHECK(before + __popc(vote & lanemask_lt()) < kDkMaxList, status, 114))
+            sList[before + __popc(vote & lanemask_lt())] = (uint16_t)c;
+        m += total;
+        __syncthreads();
+    }
+    const int nb = (m + NQ - 1) / NQ;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tDK = tmem, tS = tmem + 256;   // dK: tile * D; S: (tile * 2 + parity) * 64
+
+    if (warp < 4) {
+        // -------------------------------------------------------- loaders
+        constexpr int CPR = D / 8, RPI = 32 / CPR, CPB = SH::ROWB / 16;
+        const int chunk = lane % CPR, rsub = lane / CPR, cc = chunk % CPB;
+        const uint32_t coff = (uint32_t)(chunk / CPB) * SH::QBOX;
+        // GL lanes per query of the block; a lane's first PF list places are read ahead
+        constexpr int GL = 32 / NQ, PF = 4;
+        const int q = lane / GL, sub = lane % GL;
+        bool alive = true;
+        struct Next {
+            int t, lo, hi;   // the lane's query and its places in the block (none past the unit's queries)
+        };
+        auto look = [&](int j) {
+            const int ord = j * NQ + q;   // past the end: the last query again, counting for nothing
+            Next x{part + (int)sList[min(ord, m - 1)] * a.parts, 0, 0};
+            if (ord < m) {
+                x.lo = e0[x.t];
+                x.hi = e1[x.t];
+            }
+            return x;
+        };
+        Next nx{0, 0, 0};
+        if (warp < NS && warp < nb) nx = look(warp);
+        // warp w fills stage w every time: a stage's next filling waits for its last one's release,
+        // which a parity tells apart only for one waiter that never runs ahead
+        for (int j = warp; j < nb && warp < NS; j += NS) {
+            const int s = warp;
+            const uint32_t ph = (uint32_t)((j / NS) & 1);
+            const Next c = nx;
+            // everything this block needs from memory is asked for before the first wait
+            const int64_t base = (int64_t)(q0 + c.t) * a.l.k;
+            int key[PF];
+            float ds[PF];
+#pragma unroll
+            for (int x = 0; x < PF; ++x) {
+                const int i = c.lo + sub + x * GL;
+                key[x] = i < c.hi ? a.l.lists[base + i] - s0 : -1;
+                ds[x] = i < c.hi ? a.l.ds[base + i] : 0.f;
+            }
+            float wv[(ROWS + 31) / 32];
+#pragma unroll
+            for (int x = 0; x < (ROWS + 31) / 32; ++x) {
+                const int row = x * 32 + lane, wq = min(row / H, NQ - 1);
+                const int t = __shfl_sync(0xffffffffu, c.t, wq * GL);
+                wv[x] = row < ROWS && j * NQ + wq < m ? a.l.W[(int64_t)(q0 + t) * H + row % H] : 0.f;
+            }
+            if (j + NS < nb) nx = look(j + NS);
+            alive = tc_wait_warp(&qfree[s], ph ^ 1u, status, 41, abort_flag, alive);
+            if (!alive) break;
+            const uint32_t dst = smem_u32(sQ + s * SH::QTILE) + coff;
+#pragma unroll
+            for (int x = 0; x < ROWS / RPI; ++x) {
+                const int row = x * RPI + rsub;
+                const int t = __shfl_sync(0xffffffffu, c.t, row / H * GL);
+                const int sw = SH::ROWB == 128 ? cc ^ (row & 7) : cc ^ ((row >> 1) & 3);
+                cp_async16(dst + row * SH::ROWB + sw * 16, a.l.Q + ((int64_t)(q0 + t) * H + row % H) * D + chunk * 8);
+            }
+            cp_async_arrive(&qfull[s]);
+            alive = tc_wait_warp(&efree[s], ph ^ 1u, status, 42, abort_flag, alive);
+            if (!alive) break;
+            float* w = sW + s * 64;
+#pragma unroll
+            for (int x = 0; x < (ROWS + 31) / 32; ++x)
+                if (x * 32 + lane < ROWS) w[x * 32 + lane] = wv[x];
+            float* e = sE + s * NQ * kDkKeys;
+            for (int x = lane; x < NQ * kDkKeys / 4; x += 32)
+                reinterpret_cast<float4*>(e)[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            __syncwarp();
+            e += q * kDkKeys;
+#pragma unroll
+            for (int x = 0; x < PF; ++x)
+                if (key[x] >= 0 && DSA_CHECK(key[x] < kDkKeys, status, 115)) e[key[x]] = ds[x];
+#pragma unroll 4
+            for (int i = c.lo + sub + PF * GL; i < c.hi; i += GL) {
+                const int kk = a.l.lists[base + i] - s0;
+                if (DSA_CHECK(kk >= 0 && kk < kDkKeys, status, 115)) e[kk] = a.l.ds[base + i];
+            }
+            __syncwarp();
+            mbar_arrive(&efull[s]);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+    } else if (warp == 4) {
+        // -------------------------------------------------------- MMA issuer
+        if (lane == 0 && nb > 0) {   // (nothing listed: the epilogue writes zeros)
+            mbar_arrive_expect_tx(kfull, 2 * SH::KTILE);
+            for (int x = 0; x < 2; ++x)
+                for (int bx = 0; bx < SH::NBOX; ++bx)
+                    tma_load_2d(sK + x * SH::KTILE + bx * SH::KBOX, &tmK, bx * SH::BOXC, kb + s0 + x * 128, kfull);
+            const uint32_t idS = idesc_bf16_f32(128, ROWS);
+            const uint32_t idK = idesc_bf16_f32(128, D) | kIdescBMn;
+            bool alive = mbar_wait(kfull, 0, status, 43);
+            if (!alive) *abort_flag = 1;
+            auto flush = [&](int j) {   // dK += G . Q of block j, both tiles
+                const int s = j % NS, b = j & 1;
+                for (int x = 0; x < 2 && alive; ++x) {
+                    alive = tc_wait(&gfull[x * 2 + b], (j >> 1) & 1, status, 44, abort_flag);
+                    if (!alive) return;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < ROWS / 16; ++kk) {
+                        const uint64_t ad = smem_desc_kmajor(smem_u32(sG + (x * 2 + b) * SH::GTILE) + kk * 32, 128);
+                        const uint64_t bd = smem_desc_mnmajor(
+                            smem_u32(sQ + s * SH::QTILE) + kk * 16 * SH::ROWB, SH::ROWB, SH::QBOX);
+                        tc_mma(tDK + x * D, ad, bd, idK, kk > 0 || j > 0 ? 1u : 0u);
+                    }
+                    tc_commit(&gfree[x * 2 + b]);
+                }
+                tc_commit(&qfree[s]);
+            };
+            for (int j = 0; j < nb && alive; ++j) {
+                const int s = j % NS, b = j & 1;
+                if (!(alive = tc_wait(&qfull[s], (j / NS) & 1, status, 45, abort_flag))) break;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the copies, for the MMA's reads
+                for (int x = 0; x < 2 && alive; ++x) {
+                    alive = tc_wait(&sfree[x * 2 + b], ((j >> 1) & 1) ^ 1u, status, 46, abort_flag);
+                    if (!alive) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const int bx = kk / (SH::BOXC / 16);
+                        const uint32_t ko = (kk % (SH::BOXC / 16)) * 32;
+                        const uint64_t ad = smem_desc_kmajor(smem_u32(sK + x * SH::KTILE + bx * SH::KBOX) + ko, SH::ROWB);
+                        const uint64_t bd = smem_desc_kmajor(smem_u32(sQ + s * SH::QTILE + bx * SH::QBOX) + ko, SH::ROWB);
+                        tc_mma(tS + (x * 2 + b) * 64, ad, bd, idS, kk > 0 ? 1u : 0u);
+                    }
+                    tc_commit(&sfull[x * 2 + b]);
+                }
+                if (j > 0 && alive) flush(j - 1);
+            }
+            if (alive) flush(nb - 1);
+            tc_commit(dkfull);   // every MMA issued so far
+            mbar_wait(dkfull, 0, status, 47);
+            if (!alive) mbar_wait(kfull, 0, status, 48);   // the key tiles have landed before the CTA leaves
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------- epilogue
+        const int quarter = warp & 3, set = (warp - 5) >> 2;
+        const int lrow = quarter * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        bool alive = true;
+        for (int j = 0; j < nb; ++j) {
+            const int s = j % NS, b = j & 1, sb = set * 2 + b;
+            alive = tc_wait_warp(&efull[s], (j / NS) & 1, status, 49, abort_flag, alive);
+            alive = tc_wait_warp(&sfull[sb], (j >> 1) & 1, status, 50, abort_flag, alive);
+            if (!alive) break;
+            tc_fence_after();
+            float v[ROWS];
+            tmem_load<ROWS>(tS + sb * 64 + lanes, v);
+            tc_fence_before();
+            mbar_arrive(&sfree[sb]);
+            const float* w = sW + s * 64;
+            const float* e = sE + s * NQ * kDkKeys + set * 128 + lrow;
+            uint32_t g[ROWS / 2];
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                const float eq = e[q * kDkKeys];
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    const int c = q * H + h;
+                    v[c] = v[c] > 0.f ? eq * w[c] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < ROWS; c += 2) g[c / 2] = pack_bf16x2(v[c], v[c + 1]);
+            mbar_arrive(&efree[s]);
+            alive = tc_wait_warp(&gfree[sb], ((j >> 1) & 1) ^ 1u, status, 51, abort_flag, alive);
+            if (!alive) break;
+            uint8_t* grow = sG + sb * SH::GTILE + lrow * 128;
+#pragma unroll
+            for (int c = 0; c < ROWS / 8; ++c)
+                *reinterpret_cast<uint4*>(grow + ((c ^ (lrow & 7)) << 4)) =
+                    make_uint4(g[4 * c], g[4 * c + 1], g[4 * c + 2], g[4 * c + 3]);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            mbar_arrive(&gfull[sb]);
+        }
+        // the finished rows
+        if (nb > 0) {
+            alive = tc_wait_warp(dkfull, 0, status, 52, abort_flag, alive);
+            tc_fence_after();
+        }
+        const int key = s0 + set * 128 + lrow;
+        const int64_t row = (int64_t)kb + key;
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += 32) {
+            float v[32];
+            if (nb > 0 && alive) {
+                tmem_load<32>(tDK + set * D + c0 + lanes, v);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] = 0.f;
+            }
+            if (key < L) {
+                if (a.parts > 1) {
+                    float* out = a.part + ((int64_t)part * a.l.n_k + row) * D + c0;
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4)
+                        *reinterpret_cast<float4*>(out + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+                } else {
+                    __nv_bfloat16* out = a.l.dK + row * D + c0;
+#pragma unroll
+                    for (int c = 0; c < 32; c += 8)
+                        *reinterpret_cast<uint4*>(out + c) =
+                            make_uint4(pack_bf16x2(v[c], v[c + 1]), pack_bf16x2(v[c + 2], v[c + 3]),
+                                       pack_bf16x2(v[c + 4], v[c + 5]), pack_bf16x2(v[c + 6], v[c + 7]));
+                }
+            }
+            __syncwarp();   // the next load is the whole warp's
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 4) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// dK = the parts' sums added in order, rounded once.  n4 groups of four values.
+__global__ void __launch_bounds__(256) list_dk_join_kernel(const float4* part, int32_t parts, int64_t n4, uint2* dK)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n4) return;
+    float4 s = part[i];
+    for (int p = 1; p < parts; ++p) {
+        const float4 v = part[p * n4 + i];
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+    dK[i] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+}
+
+}  // namespace dsa

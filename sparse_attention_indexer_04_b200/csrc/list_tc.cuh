@@ -1,7 +1,7 @@
 // Indexer scores at listed keys and their backward pass on the tensor cores (tcgen05 / TMEM).
 //
-// One query at a time per CTA: its listed keys pass by in tiles of 128, gathered by TMA
-// (four rows per instruction), and
+// One query at a time per CTA: its listed keys pass by in tiles of 128, gathered by
+// asynchronous copies, and
 //   S[128 keys x HP heads] = K_tile . Q^T                 (A = keys, B = heads, both K-major over d)
 //   scores: s[j] = sum_h w_h max(0, S[j,h])               (registers; one key per thread)
 //   backward, with e = ds[j]:
@@ -10,20 +10,20 @@
 //     dW_h = sum_j e max(0, S[j,h])                       (fp32 registers, joined once per query)
 // The tile is read once for both products, so a query moves its listed keys from L2 exactly once;
 // that gather (256 bytes per listed pair at d = 128) is what bounds the kernel, not the products.
-// Roles: warps 0, 10, 11 gather; warp 1 issues the MMAs; warps 2..9 are two sets of four that take
+// Roles: warps 0, 10..12 gather; warp 1 issues the MMAs; warps 2..9 are two sets of four that take
 // alternate tiles (one S buffer each), so one set computes while the other's product runs.
 // HP = max(16, H): heads above H have zero rows in the query tile.  Every wait is bounded.
 #pragma once
 
 #include <math_constants.h>
 
-#include "list_simt.cuh"
+#include "list.cuh"
 #include "ptx.cuh"
 
 namespace dsa {
 
-constexpr int kListTcThreads = 384;
-constexpr int kListTcProducers = 3;
+constexpr int kListTcThreads = 416;
+constexpr int kListTcProducers = 4;
 constexpr uint32_t kErrListAlign = 3;
 
 // Shared-memory matrix descriptor of an MN-major operand: rows of the K dimension are row_bytes
@@ -79,6 +79,18 @@ __device__ __forceinline__ bool tc_wait_warp(uint64_t* bar, uint32_t parity, uin
 __device__ __forceinline__ void named_barrier(int id, int threads)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Copies 16 bytes to shared memory, past L1.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// One of the barrier's expected arrivals, made when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
@@ -141,11 +153,9 @@ __device__ __forceinline__ void warp_transpose_sum(float* v, int lane)
 
 template <int D, int HP, bool BWD>
 __global__ void __launch_bounds__(kListTcThreads, 1)
-    list_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmKg,
-                   const __grid_constant__ ListTcArgs a)
+    list_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ ListTcArgs a)
 {
     using SH = ListShape<D, HP>;
-    constexpr int NP = kListTcProducers;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint32_t* status = a.l.status;
     if (smem_u32(smem) & 1023u) {
@@ -159,7 +169,7 @@ __global__ void __launch_bounds__(kListTcThreads, 1)
     float* sW = reinterpret_cast<float*>(smem + SH::w_off(n_stages));
     float* sDW = sW + SH::W_BYTES / 4;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + SH::w_off(n_stages) + SH::W_BYTES + SH::DW_BYTES);
-    uint64_t* kempty = full + NP * n_stages;   // the tile's products have read it
+    uint64_t* kempty = full + n_stages;   // the tile's products have read it
     uint64_t* qfull = kempty + n_stages;       // [2] the query tile has landed
     uint64_t* qempty = qfull + 2;              // [2] its last product has read it
     uint64_t* sfull = qempty + 2;              // [2] S is complete
@@ -174,7 +184,7 @@ __global__ void __launch_bounds__(kListTcThreads, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < NP * n_stages; ++i) mbar_init(&full[i], 1);
+        for (int i = 0; i < n_stages; ++i) mbar_init(&full[i], kListTcProducers * 32);
         for (int i = 0; i < n_stages; ++i) mbar_init(&kempty[i], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&qfull[i], 1);
@@ -190,7 +200,6 @@ __global__ void __launch_bounds__(kListTcThreads, 1)
         *abort_flag = 0;
         fence_barrier_init();
         prefetch_tensormap(&tmQ);
-        prefetch_tensormap(&tmKg);
     }
     // heads above H: zero rows that no load overwrites
     for (uint32_t i = threadIdx.x; i < SH::align1k(2 * SH::QTILE) / 4; i += kListTcThreads)
@@ -208,17 +217,18 @@ __global__ void __launch_bounds__(kListTcThreads, 1)
 
     if (warp == 0 || warp >= 10) {
         // ------------------------------------------------------ producers
+        // Four warps of 32 tile rows each, 16 bytes a lane (asynchronous copies, two rows of 256 bytes
+        // an instruction at d = 128).  Gathering the same tile with TMA (gather4) took 2400 clocks.
         const int pw = warp == 0 ? 0 : warp - 9;
-        constexpr int kItems = 32 * SH::NBOX;
-        const int w = lane * NP + pw;
-        const bool has_item = w < kItems;
-        const int rg = w % 32, ibox = w / 32;
-        const uint32_t my_bytes = (uint32_t)((kItems - pw + NP - 1) / NP) * 4 * SH::ROWB;
-        uint64_t* my_full = full + pw * n_stages;
-        const uint64_t keep_keys = l2_policy_evict_last();
+        constexpr int CPR = D / 8;             // 16-byte chunks of a row
+        constexpr int RPI = 32 / CPR;          // rows per instruction
+        constexpr int CPB = SH::ROWB / 16;     // chunks of a box row
+        const int chunk = lane % CPR, rsub = lane / CPR;
+        const uint32_t coff = (uint32_t)(chunk / CPB) * SH::KBOX;
+        const int cc = chunk % CPB;
+        const uint32_t sk = smem_u32(sK);
         int stage = 0, it = 0;
         uint32_t phase = 0;
-        int issued = 0;
         int q_issued = 0;
         bool alive = true;
         RowDesc nx = (int)blockIdx.x < n_q ? a.l.rows[blockIdx.x] : none;
@@ -228,6 +238,9 @@ __global__ void __launch_bounds__(kListTcThreads, 1)
             const int nt = (r.ncols + 127) >> 7;
             if (nt == 0) continue;
             const int qb = it & 1;
+            const int32_t* l = a.l.lists + (int64_t)t * k + pw * 32 + lane;
+            const int last = r.ncols - 1 - pw * 32 - lane;   // places behind the last take its key again
+            int key = __ldg(l + min(0, last));
             if (pw == 0) {
                 int ok = 1;
                 if (lane == 0) {
@@ -242,50 +255,32 @@ __global__ void __launch_bounds__(kListTcThreads, 1)
                 ++q_issued;
             }
             ++it;
-            const int32_t* l = a.l.lists + (int64_t)t * k;
-            const int krow0 = a.l.k_off[r.seq];
-            const bool list4 = (reinterpret_cast<uintptr_t>(l) & 15) == 0;
-            auto tile_rows = [&](int i, int (&y)[4]) {
-                const int c0 = i * 128 + 4 * rg;
-                if (c0 + 3 < r.ncols && list4) {
-                    const int4 v = __ldg(reinterpret_cast<const int4*>(l + c0));
-                    y[0] = krow0 + v.x; y[1] = krow0 + v.y; y[2] = krow0 + v.z; y[3] = krow0 + v.w;
-                } else {   // places behind the last take its key again
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = krow0 + __ldg(l + min(c0 + e, r.ncols - 1));
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (!DSA_CHECK(y[e] >= 0 && y[e] < a.l.n_k, status, 113)) y[e] = 0;
-            };
-            int ynext[4] = {0, 0, 0, 0};
-            if (has_item) tile_rows(0, ynext);
+            const __nv_bfloat16* kbase = a.l.K + (int64_t)a.l.k_off[r.seq] * D + chunk * 8;
+            [[maybe_unused]] const int n_seq = a.l.k_off[r.seq + 1] - a.l.k_off[r.seq];
             for (int i = 0; i < nt; ++i) {
-                int ok = 1;
-                if (lane == 0) ok = tc_wait(&kempty[stage], phase ^ 1u, status, 22, abort_flag) ? 1 : 0;
-                if (!__shfl_sync(0xffffffffu, ok, 0)) { alive = false; break; }
-                if (lane == 0) mbar_arrive_expect_tx(&my_full[stage], my_bytes);
-                __syncwarp();
-                if (has_item) {
-                    const int y[4] = {ynext[0], ynext[1], ynext[2], ynext[3]};
-                    tma_gather4_2d_hint(sK + stage * SH::KTILE + ibox * SH::KBOX + 4 * rg * SH::ROWB, &tmKg,
-                                        ibox * SH::BOXC, y[0], y[1], y[2], y[3], &my_full[stage], keep_keys);
-                    if (i + 1 < nt) tile_rows(i + 1, ynext);
+                const int mine = DSA_CHECK(key >= 0 && key < n_seq, status, 113) ? key : 0;
+                if (i + 1 < nt) key = __ldg(l + min((i + 1) * 128, last));
+                alive = tc_wait_warp(&kempty[stage], phase ^ 1u, status, 22, abort_flag, alive);
+                if (!alive) break;
+                const uint32_t tile = sk + stage * SH::KTILE + coff;
+#pragma unroll
+                for (int x = 0; x < 32 / RPI; ++x) {
+                    const int row = pw * 32 + x * RPI + rsub;
+                    const int s = __shfl_sync(0xffffffffu, mine, x * RPI + rsub);
+                    const int sw = SH::ROWB == 128 ? cc ^ (row & 7) : cc ^ ((row >> 1) & 3);
+                    cp_async16(tile + row * SH::ROWB + sw * 16, kbase + (int64_t)s * D);
                 }
-                ++issued;
+                cp_async_arrive(&full[stage]);
                 if (++stage == n_stages) { stage = 0; phase ^= 1u; }
             }
         }
-        if (lane == 0 && *abort_flag) {   // every copy this warp started must have landed
+        // every copy this warp started lands before the CTA leaves
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (pw == 0 && lane == 0 && *abort_flag)
             for (int back = 1; back <= 2 && back <= q_issued; ++back) {
                 const int i = q_issued - back;
                 mbar_wait(&qfull[i & 1], (uint32_t)((i >> 1) & 1), status, 23);
             }
-            for (int back = 1; back <= n_stages && back <= issued; ++back) {
-                const int i = issued - back;
-                mbar_wait(&my_full[i % n_stages], (uint32_t)((i / n_stages) & 1), status, 24);
-            }
-        }
         __syncwarp();
     } else if (warp == 1) {
         // -------------------------------------------------------- MMA issuer
@@ -330,9 +325,8 @@ __global__ void __launch_bounds__(kListTcThreads, 1)
                 if (!tc_wait(&qfull[qb], (it >> 1) & 1, status, 27, abort_flag)) break;
                 for (int i = 0; i < nt && alive; ++i, ++n) {
                     const int b = n & 1;
-                    for (int p = 0; p < NP && alive; ++p)
-                        alive = tc_wait(&full[p * n_stages + stage], phase, status, 28, abort_flag);
-                    if (!alive) break;
+                    if (!tc_wait(&full[stage], phase, status, 28, abort_flag)) { alive = false; break; }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the copies, for the MMA's reads
                     if (!tc_wait(&sfree[b], ((n >> 1) & 1) ^ 1u, status, 29, abort_flag)) { alive = false; break; }
                     tc_fence_after();
 #pragma unroll

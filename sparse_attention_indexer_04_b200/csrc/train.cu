@@ -8,7 +8,7 @@
 #include "../../include/dsa_index.h"
 #include "distill.cuh"
 #include "host.cuh"
-#include "list_simt.cuh"
+#include "list_dk_tc.cuh"
 #include "list_tc.cuh"
 #include "norm.cuh"
 
@@ -131,14 +131,34 @@ dsa_status distill_pick(const DistillArgs& a, cudaStream_t st)
 
 struct ListPlan {
     RowDesc* rows;
+    uint16_t* edge;     // backward: list places at the borders of the key blocks
+    float* part;        // backward: partial dK of the query parts
+    int32_t key_blocks; // of the longest sequence
+    int32_t units;      // key blocks over all sequences (an upper bound)
+    int32_t parts;
 };
 
-size_t list_plan(char* base, const dsa_batch* b, int32_t k, bool backward, ListPlan* p)
+// CTAs that share a key block's queries: enough for three waves over the GPU (a block's work is its
+// queries', so early blocks of a causal sequence have the most), no more than there are groups of 16
+// queries, and enough that a CTA's queries fit its list.
+int32_t dk_parts(int32_t units, int32_t max_q)
 {
-    (void)k;
-    (void)backward;
+    const int32_t fill = (3 * 148 + units - 1) / std::max(1, units);
+    const int32_t most = std::max(1, std::min(32, max_q / 16));
+    return std::max((max_q + kDkMaxList - 1) / kDkMaxList, std::max(1, std::min(fill, most)));
+}
+
+size_t list_plan(char* base, const dsa_batch* b, const HostInfo& hi, bool backward, ListPlan* p)
+{
     Carver c{base};
+    *p = ListPlan{};
     p->rows = c.take<RowDesc>(std::max(1, b->num_queries));
+    if (!backward) return c.off;
+    p->key_blocks = (hi.max_k + kDkKeys - 1) / kDkKeys;
+    p->units = b->num_keys / kDkKeys + b->num_seqs;
+    p->parts = dk_parts(p->units, hi.max_q);
+    p->edge = c.take<uint16_t>(size_t(p->key_blocks + 1) * std::max(1, b->num_queries));
+    if (p->parts > 1) p->part = c.take<float>(size_t(p->parts) * b->num_keys * b->head_dim);
     return c.off;
 }
 
@@ -185,15 +205,14 @@ template <int D, int HP, bool BWD>
 dsa_status list_tc_launch(const ListArgs& l, cudaStream_t st)
 {
     using SH = ListShape<D, HP>;
-    CUtensorMap mq, mk;
-    if (!make_tile_map(&mq, l.Q, int64_t(l.n_q) * l.H, D, l.H) || !make_tile_map(&mk, l.n_k > 0 ? l.K : l.Q, l.n_k > 0 ? l.n_k : l.n_q, D, 1))   // (no keys: never read)
-        return DSA_ERR_CUDA;
+    CUtensorMap mq;
+    if (!make_tile_map(&mq, l.Q, int64_t(l.n_q) * l.H, D, l.H)) return DSA_ERR_CUDA;
     ListTcArgs a{l, std::min(8, int((kSmemMax - SH::bytes(0)) / SH::KTILE))};
     const int smem = std::max<int>(SH::bytes(a.n_stages), 120 * 1024);   // one CTA an SM
     dsa_status s = set_smem(list_tc_kernel<D, HP, BWD>, smem);
     if (s != DSA_OK) return s;
-    DSA_LAUNCH(BWD ? kProfListGrad : kProfListScores, st,
-               launch_pdl(true, list_tc_kernel<D, HP, BWD>, std::min(l.n_q, 148), kListTcThreads, smem, st, mq, mk, a));
+    DSA_LAUNCH(BWD ? kProfListDq : kProfListScores, st,
+               launch_pdl(true, list_tc_kernel<D, HP, BWD>, std::min(l.n_q, 148), kListTcThreads, smem, st, mq, a));
     return launched();
 }
 
@@ -211,21 +230,50 @@ dsa_status list_scores_d(const ListArgs& a, cudaStream_t st)
     return list_tc<D, false>(a, st);
 }
 
-template <int D>
-dsa_status list_backward_d(const ListArgs& a, cudaStream_t st)
+template <int D, int H>
+dsa_status list_dk_launch(const ListArgs& l, const ListPlan& p, cudaStream_t st)
 {
-    const size_t smem = (size_t(a.H) * D + kListTile * (D + 1) + kListTile * a.H) * 4;
+    using SH = DkShape<D, H>;
+    CUtensorMap mk;
+    if (!make_tile_map(&mk, l.K, l.n_k, D, 128)) return DSA_ERR_CUDA;
+    const DkArgs a{l, p.edge, p.part, p.parts};
+    const int smem = std::max<int>(SH::bytes, 120 * 1024);   // one CTA an SM: each takes all of TMEM
+    dsa_status s = set_smem(list_dk_tc_kernel<D, H>, smem);
+    if (s != DSA_OK) return s;
+    DSA_LAUNCH(kProfListDk, st, list_dk_tc_kernel<D, H><<<(unsigned)p.units * p.parts, kDkThreads, smem, st>>>(mk, a));
+    if ((s = launched()) != DSA_OK || p.parts == 1) return s;
+    const int64_t n4 = int64_t(l.n_k) * D / 4;
+    DSA_LAUNCH(kProfListDk, st, list_dk_join_kernel<<<(unsigned)((n4 + 255) / 256), 256, 0, st>>>(
+        reinterpret_cast<const float4*>(p.part), p.parts, n4, reinterpret_cast<uint2*>(l.dK)));
+    return launched();
+}
+
+template <int D>
+dsa_status list_dk(const ListArgs& a, const ListPlan& p, cudaStream_t st)
+{
+    switch (a.H) {
+    case 1: return list_dk_launch<D, 1>(a, p, st);
+    case 2: return list_dk_launch<D, 2>(a, p, st);
+    case 4: return list_dk_launch<D, 4>(a, p, st);
+    case 8: return list_dk_launch<D, 8>(a, p, st);
+    case 16: return list_dk_launch<D, 16>(a, p, st);
+    case 32: return list_dk_launch<D, 32>(a, p, st);
+    default: return list_dk_launch<D, 64>(a, p, st);
+    }
+}
+
+template <int D>
+dsa_status list_backward_d(const ListArgs& a, const ListPlan& p, cudaStream_t st)
+{
     dsa_status s;
-    if (a.n_q > 0 && (a.dQ || a.dW)) {
-        if ((s = list_tc<D, true>(a, st)) != DSA_OK) return s;
-    }
-    if (a.n_k > 0 && a.dK) {
-        if ((s = set_smem(list_dk_simt_kernel<D>, smem)) != DSA_OK) return s;
-        DSA_LAUNCH(kProfListGrad, st,
-                   list_dk_simt_kernel<D><<<(a.n_k + kListTile - 1) / kListTile, kListThreads, smem, st>>>(a));
-        if ((s = launched()) != DSA_OK) return s;
-    }
-    return DSA_OK;
+    if (a.n_q > 0 && (a.dQ || a.dW) && (s = list_tc<D, true>(a, st)) != DSA_OK) return s;
+    if (a.n_k == 0 || !a.dK) return DSA_OK;
+    if (a.n_q == 0)   // nothing lists a key
+        return cudaMemsetAsync(a.dK, 0, size_t(a.n_k) * D * 2, st) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+    DSA_LAUNCH(kProfSetup, st, list_edges_kernel<<<(a.n_q + 7) / 8, 256, 0, st>>>(a.lists, a.k, a.rows, a.n_q,
+                                                                                  p.key_blocks, p.edge));
+    if ((s = launched()) != DSA_OK) return s;
+    return list_dk<D>(a, p, st);
 }
 
 }  // namespace
@@ -336,7 +384,7 @@ size_t dsa_list_scores_workspace(const dsa_batch* b, int32_t k)
 {
     HostInfo hi;
     ListPlan p;
-    return list_check(b, &hi, k) == DSA_OK ? list_plan(nullptr, b, k, false, &p) : 0;
+    return list_check(b, &hi, k) == DSA_OK ? list_plan(nullptr, b, hi, false, &p) : 0;
 }
 
 dsa_status dsa_list_scores(const dsa_batch* b, const void* Q, const void* K, const float* W, int32_t k,
@@ -349,8 +397,8 @@ dsa_status dsa_list_scores(const dsa_batch* b, const void* Q, const void* K, con
     if (b->num_queries > 0 && (!lists || !scores)) return DSA_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(lists) | reinterpret_cast<uintptr_t>(scores)) & 3) return DSA_ERR_INVALID_ARG;
     ListPlan p;
-    if ((s = check_ws(ws, ws_bytes, list_plan(nullptr, b, k, false, &p))) != DSA_OK) return s;
-    list_plan(static_cast<char*>(ws), b, k, false, &p);
+    if ((s = check_ws(ws, ws_bytes, list_plan(nullptr, b, hi, false, &p))) != DSA_OK) return s;
+    list_plan(static_cast<char*>(ws), b, hi, false, &p);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if ((s = list_rows(b, k, lists, p, ws, st)) != DSA_OK || b->num_queries == 0) return s;
     ListArgs a = list_args(b, Q, K, W, k, lists, p, ws);
@@ -366,7 +414,7 @@ size_t dsa_list_scores_backward_workspace(const dsa_batch* b, int32_t k)
 {
     HostInfo hi;
     ListPlan p;
-    return list_check(b, &hi, k) == DSA_OK ? list_plan(nullptr, b, k, true, &p) : 0;
+    return list_check(b, &hi, k) == DSA_OK ? list_plan(nullptr, b, hi, true, &p) : 0;
 }
 
 dsa_status dsa_list_scores_backward(const dsa_batch* b, const void* Q, const void* K, const float* W, int32_t k,
@@ -382,8 +430,8 @@ dsa_status dsa_list_scores_backward(const dsa_batch* b, const void* Q, const voi
         return DSA_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(dQ) | reinterpret_cast<uintptr_t>(dK)) & 15) return DSA_ERR_INVALID_ARG;
     ListPlan p;
-    if ((s = check_ws(ws, ws_bytes, list_plan(nullptr, b, k, true, &p))) != DSA_OK) return s;
-    list_plan(static_cast<char*>(ws), b, k, true, &p);
+    if ((s = check_ws(ws, ws_bytes, list_plan(nullptr, b, hi, true, &p))) != DSA_OK) return s;
+    list_plan(static_cast<char*>(ws), b, hi, true, &p);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if ((s = list_rows(b, k, lists, p, ws, st)) != DSA_OK) return s;
     ListArgs a = list_args(b, Q, K, W, k, lists, p, ws);
@@ -392,9 +440,9 @@ dsa_status dsa_list_scores_backward(const dsa_batch* b, const void* Q, const voi
     a.dK = static_cast<__nv_bfloat16*>(dK);
     a.dW = dW;
     switch (b->head_dim) {
-    case 32: return list_backward_d<32>(a, st);
-    case 64: return list_backward_d<64>(a, st);
-    default: return list_backward_d<128>(a, st);
+    case 32: return list_backward_d<32>(a, p, st);
+    case 64: return list_backward_d<64>(a, p, st);
+    default: return list_backward_d<128>(a, p, st);
     }
 }
 
