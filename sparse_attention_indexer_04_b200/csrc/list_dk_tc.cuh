@@ -13,14 +13,15 @@
 // a tenth of the prefix.  The queries of a sequence are dealt to `parts` CTAs per key block when there
 // are few key blocks; their fp32 partial sums are added in order by a second kernel.
 // Roles: warps 0..3 load (one stage each: query rows, weights and the block's ds), warp 4 issues
-// the MMAs, warps 5..12 are two sets of four, one per key tile.  Every wait is bounded.
+// the MMAs, warps 5..20 are four sets of four: a key tile and half of the query-head rows each (one
+// set a tile left the kernel bound by the latency of a block's epilogue).  Every wait is bounded.
 #pragma once
 
 #include "list_tc.cuh"
 
 namespace dsa {
 
-constexpr int kDkThreads = 416;
+constexpr int kDkThreads = 672;
 constexpr int kDkKeys = 256;
 constexpr int kDkMaxList = 8192;   // queries of one CTA at most
 
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(kDkThreads, 1)
     uint64_t* dkfull = gfree + 4;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dkfull + 1);
     volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
-    int32_t* sCount = reinterpret_cast<int32_t*>(tmem_slot + 2);   // [14] per-warp counts, then the total
+    int32_t* sCount = reinterpret_cast<int32_t*>(tmem_slot + 2);   // [21] per-warp counts
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -130,12 +131,12 @@ __global__ void __launch_bounds__(kDkThreads, 1)
             mbar_init(&qfull[i], 32);
             mbar_init(&qfree[i], 1);
             mbar_init(&efull[i], 32);
-            mbar_init(&efree[i], 256);
+            mbar_init(&efree[i], 512);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&sfull[i], 1);
-            mbar_init(&sfree[i], 128);
-            mbar_init(&gfull[i], 128);
+            mbar_init(&sfree[i], 256);
+            mbar_init(&gfull[i], 256);
             mbar_init(&gfree[i], 1);
         }
         mbar_init(dkfull, 1);
@@ -311,41 +312,44 @@ __global__ void __launch_bounds__(kDkThreads, 1)
         __syncwarp();
     } else {
         // ---------------------------------------------------------- epilogue
-        const int quarter = warp & 3, set = (warp - 5) >> 2;
+        const int quarter = warp & 3, set = (warp - 5) >> 3, half = ((warp - 5) >> 2) & 1;
         const int lrow = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        constexpr int NC = ROWS / 2;   // query-head rows (columns of S) of a set
+        const int c0 = half * NC;
         bool alive = true;
         for (int j = 0; j < nb; ++j) {
             const int s = j % NS, b = j & 1, sb = set * 2 + b;
             alive = tc_wait_warp(&efull[s], (j / NS) & 1, status, 49, abort_flag, alive);
+            const float* e = sE + (s * NQ + (NQ > 1 ? half * (NQ / 2) : 0)) * kDkKeys + set * 128 + lrow;
+            float eq[NQ > 1 ? NQ / 2 : 1];
+#pragma unroll
+            for (int q = 0; q < (NQ > 1 ? NQ / 2 : 1); ++q) eq[q] = alive ? e[q * kDkKeys] : 0.f;
             alive = tc_wait_warp(&sfull[sb], (j >> 1) & 1, status, 50, abort_flag, alive);
             if (!alive) break;
             tc_fence_after();
-            float v[ROWS];
-            tmem_load<ROWS>(tS + sb * 64 + lanes, v);
+            float v[NC];
+            tmem_load<NC>(tS + sb * 64 + c0 + lanes, v);
             tc_fence_before();
             mbar_arrive(&sfree[sb]);
-            const float* w = sW + s * 64;
-            const float* e = sE + s * NQ * kDkKeys + set * 128 + lrow;
-            uint32_t g[ROWS / 2];
+            const float* w = sW + s * 64 + c0;
+            uint32_t g[NC / 2];
 #pragma unroll
-            for (int q = 0; q < NQ; ++q) {
-                const float eq = e[q * kDkKeys];
+            for (int c = 0; c < NC; c += 4) {
+                const float4 w4 = *reinterpret_cast<const float4*>(w + c);
+                const float wv[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    const int c = q * H + h;
-                    v[c] = v[c] > 0.f ? eq * w[c] : 0.f;
-                }
+                for (int x = 0; x < 4; ++x) v[c + x] = v[c + x] > 0.f ? eq[NQ > 1 ? (c + x) / H : 0] * wv[x] : 0.f;
+                g[c / 2] = pack_bf16x2(v[c], v[c + 1]);
+                g[c / 2 + 1] = pack_bf16x2(v[c + 2], v[c + 3]);
             }
-#pragma unroll
-            for (int c = 0; c < ROWS; c += 2) g[c / 2] = pack_bf16x2(v[c], v[c + 1]);
             mbar_arrive(&efree[s]);
             alive = tc_wait_warp(&gfree[sb], ((j >> 1) & 1) ^ 1u, status, 51, abort_flag, alive);
             if (!alive) break;
             uint8_t* grow = sG + sb * SH::GTILE + lrow * 128;
 #pragma unroll
-            for (int c = 0; c < ROWS / 8; ++c)
-                *reinterpret_cast<uint4*>(grow + ((c ^ (lrow & 7)) << 4)) =
+            for (int c = 0; c < NC / 8; ++c)
+                *reinterpret_cast<uint4*>(grow + (((half * (NC / 8) + c) ^ (lrow & 7)) << 4)) =
                     make_uint4(g[4 * c], g[4 * c + 1], g[4 * c + 2], g[4 * c + 3]);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             mbar_arrive(&gfull[sb]);
@@ -358,24 +362,25 @@ __global__ void __launch_bounds__(kDkThreads, 1)
         const int key = s0 + set * 128 + lrow;
         const int64_t row = (int64_t)kb + key;
 #pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 32) {
-            float v[32];
+        for (int x0 = 0; x0 < D / 2; x0 += 16) {   // each set half of the dimensions
+            const int x = half * (D / 2) + x0;
+            float v[16];
             if (nb > 0 && alive) {
-                tmem_load<32>(tDK + set * D + c0 + lanes, v);
+                tmem_load<16>(tDK + set * D + x + lanes, v);
             } else {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) v[c] = 0.f;
+                for (int c = 0; c < 16; ++c) v[c] = 0.f;
             }
             if (key < L) {
                 if (a.parts > 1) {
-                    float* out = a.part + ((int64_t)part * a.l.n_k + row) * D + c0;
+                    float* out = a.part + ((int64_t)part * a.l.n_k + row) * D + x;
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4)
+                    for (int c = 0; c < 16; c += 4)
                         *reinterpret_cast<float4*>(out + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
                 } else {
-                    __nv_bfloat16* out = a.l.dK + row * D + c0;
+                    __nv_bfloat16* out = a.l.dK + row * D + x;
 #pragma unroll
-                    for (int c = 0; c < 32; c += 8)
+                    for (int c = 0; c < 16; c += 8)
                         *reinterpret_cast<uint4*>(out + c) =
                             make_uint4(pack_bf16x2(v[c], v[c + 1]), pack_bf16x2(v[c + 2], v[c + 3]),
                                        pack_bf16x2(v[c + 4], v[c + 5]), pack_bf16x2(v[c + 6], v[c + 7]));

@@ -10,8 +10,8 @@
 //     dW_h = sum_j e max(0, S[j,h])                       (fp32 registers, joined once per query)
 // The tile is read once for both products, so a query moves its listed keys from L2 exactly once;
 // that gather (256 bytes per listed pair at d = 128) is what bounds the kernel, not the products.
-// Roles: warps 0, 10..12 gather; warp 1 issues the MMAs; warps 2..9 are two sets of four that take
-// alternate tiles (one S buffer each), so one set computes while the other's product runs.
+// Roles: warp 0 and the last three gather; warp 1 issues the MMAs; the warps between them are the
+// epilogue.  S is double-buffered, so a tile's product runs while the tile before is worked on.
 // HP = max(16, H): heads above H have zero rows in the query tile.  Every wait is bounded.
 #pragma once
 
@@ -22,8 +22,12 @@
 
 namespace dsa {
 
-constexpr int kListTcThreads = 416;
+// Epilogue warps: forward two sets of four on alternate tiles; backward four sets of four on each tile,
+// a quarter of the heads each (one set a tile left the kernel bound by the latency of a tile's epilogue
+// at 2600 clocks, 64 heads a thread).
 constexpr int kListTcProducers = 4;
+constexpr int list_sets(bool bwd) { return bwd ? 4 : 2; }
+constexpr int list_threads(bool bwd) { return 32 * (1 + kListTcProducers) + 128 * list_sets(bwd); }
 constexpr uint32_t kErrListAlign = 3;
 
 // Shared-memory matrix descriptor of an MN-major operand: rows of the K dimension are row_bytes
@@ -55,11 +59,35 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v)
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// N (16, 32 or 64) consecutive columns of this thread's TMEM lane; waits for them.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v)
+{
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, float* v)
+{
+    uint32_t r[4];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// N (4, 8, 16, 32 or 64) consecutive columns of this thread's TMEM lane; waits for them.
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t taddr, float* v)
 {
-    if constexpr (N == 16) {
+    if constexpr (N == 4) {
+        tmem_ld4(taddr, v);
+    } else if constexpr (N == 8) {
+        tmem_ld8(taddr, v);
+    } else if constexpr (N == 16) {
         tmem_ld16(taddr, v);
     } else {
 #pragma unroll
@@ -110,8 +138,8 @@ struct ListShape {
     static constexpr uint32_t QBOX = (uint32_t)HP * ROWB;
     static constexpr uint32_t QTILE = QBOX * NBOX;
     static constexpr uint32_t GTILE = 128u * 128u;   // rows of 128 bytes, the first HP heads used
-    static constexpr uint32_t W_BYTES = 2u * 2u * HP * 4;         // [set][parity][head]
-    static constexpr uint32_t DW_BYTES = 2u * 8u * HP * 4;        // [parity][warp][head]
+    static constexpr uint32_t W_BYTES = 4u * 2u * HP * 4;         // [set][parity][head]
+    static constexpr uint32_t DW_BYTES = 2u * 4u * HP * 4;        // [parity][warp of the set][head]
     static constexpr uint32_t BAR_BYTES = 512;
     static constexpr uint32_t align1k(uint32_t x) { return (x + 1023u) & ~1023u; }
     // key stages, query tiles, G tiles, then the small arrays.  An operand tile narrower than the
@@ -127,32 +155,27 @@ struct ListTcArgs {
     int32_t n_stages;
 };
 
-// Sums 32 / 64 per-lane values over the warp: lane i ends with the sums of values i (and i + 32).
-// A butterfly that halves the number of values at each step: N values cost about N + N/2 shuffles.
+// Sums N (at most 16) per-lane values over the warp: lane i < N ends with the sum of value i in v[0].
+// Each step halves the number of values, so N values cost about N shuffles.
 template <int N>
 __device__ __forceinline__ void warp_transpose_sum(float* v, int lane)
 {
-    if constexpr (N == 64) {
-        // two interleaved halves of 32
-        warp_transpose_sum<32>(v, lane);
-        warp_transpose_sum<32>(v + 32, lane);
-    } else {
 #pragma unroll
-        for (int o = N / 2; o > 0; o >>= 1) {
-            const bool up = lane & o;
+    for (int o = N / 2; o > 0; o >>= 1) {
+        const bool up = lane & o;
 #pragma unroll
-            for (int i = 0; i < o; ++i) {
-                const float send = up ? v[i] : v[i + o];
-                const float keep = up ? v[i + o] : v[i];
-                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-            }
+        for (int i = 0; i < o; ++i) {
+            const float send = up ? v[i] : v[i + o];
+            const float keep = up ? v[i + o] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
         }
-        if constexpr (N == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
     }
+#pragma unroll
+    for (int o = N; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
 }
 
 template <int D, int HP, bool BWD>
-__global__ void __launch_bounds__(kListTcThreads, 1)
+__global__ void __launch_bounds__(list_threads(BWD), 1)
     list_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ ListTcArgs a)
 {
     using SH = ListShape<D, HP>;
@@ -182,6 +205,7 @@ __global__ void __launch_bounds__(kListTcThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
 
+    constexpr int kEpi = 4 * list_sets(BWD);   // epilogue warps 2 .. kEpi + 1
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < n_stages; ++i) mbar_init(&full[i], kListTcProducers * 32);
@@ -190,11 +214,11 @@ __global__ void __launch_bounds__(kListTcThreads, 1)
             mbar_init(&qfull[i], 1);
             mbar_init(&qempty[i], 1);
             mbar_init(&sfull[i], 1);
-            mbar_init(&sfree[i], 128);
-            mbar_init(&gfull[i], 128);
+            mbar_init(&sfree[i], BWD ? 512 : 128);
+            mbar_init(&gfull[i], 512);
             mbar_init(&gfree[i], 1);
             mbar_init(&dqfull[i], 1);
-            mbar_init(&dqfree[i], 256);
+            mbar_init(&dqfree[i], 512);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -202,7 +226,7 @@ __global__ void __launch_bounds__(kListTcThreads, 1)
         prefetch_tensormap(&tmQ);
     }
     // heads above H: zero rows that no load overwrites
-    for (uint32_t i = threadIdx.x; i < SH::align1k(2 * SH::QTILE) / 4; i += kListTcThreads)
+    for (uint32_t i = threadIdx.x; i < SH::align1k(2 * SH::QTILE) / 4; i += list_threads(BWD))
         reinterpret_cast<uint32_t*>(sQ)[i] = 0u;
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     if (warp == 1) tmem_alloc(tmem_slot, 256);
@@ -215,11 +239,11 @@ __global__ void __launch_bounds__(kListTcThreads, 1)
     const int n_q = a.l.n_q, H = a.l.H, k = a.l.k, step = gridDim.x;
     const RowDesc none{0, 0, 0, 0};
 
-    if (warp == 0 || warp >= 10) {
+    if (warp == 0 || warp >= 2 + kEpi) {
         // ------------------------------------------------------ producers
         // Four warps of 32 tile rows each, 16 bytes a lane (asynchronous copies, two rows of 256 bytes
         // an instruction at d = 128).  Gathering the same tile with TMA (gather4) took 2400 clocks.
-        const int pw = warp == 0 ? 0 : warp - 9;
+        const int pw = warp == 0 ? 0 : warp - 1 - kEpi;
         constexpr int CPR = D / 8;             // 16-byte chunks of a row
         constexpr int RPI = 32 / CPR;          // rows per instruction
         constexpr int CPB = SH::ROWB / 16;     // chunks of a box row
@@ -384,25 +408,17 @@ __global__ void __launch_bounds__(kListTcThreads, 1)
             }
             named_barrier(1 + set, 128);
             const int nt = (r.ncols + 127) >> 7;
-            [[maybe_unused]] float dw[HP];
-            if constexpr (BWD) {
-#pragma unroll
-                for (int h = 0; h < HP; ++h) dw[h] = 0.f;
-            }
-            int i = (n & 1) == set ? 0 : 1;   // the set's first tile
-            float e = 0.f;
-            if (BWD && i * 128 + lrow < r.ncols) e = a.l.ds[(int64_t)t * k + i * 128 + lrow];
-            for (; i < nt; i += 2) {
-                const int g = n + i;   // the CTA's tile number
-                alive = tc_wait_warp(&sfull[set], (g >> 1) & 1, status, 31, abort_flag, alive);
-                if (!alive) continue;
-                tc_fence_after();
-                float v[HP];
-                tmem_load<HP>(tS + set * 64 + lanes, v);
-                tc_fence_before();
-                mbar_arrive(&sfree[set]);
-                const int j = i * 128 + lrow;
-                if constexpr (!BWD) {
+            if constexpr (!BWD) {
+                for (int i = (n & 1) == set ? 0 : 1; i < nt; i += 2) {   // the set's tiles
+                    const int g = n + i;   // the CTA's tile number
+                    alive = tc_wait_warp(&sfull[set], (g >> 1) & 1, status, 31, abort_flag, alive);
+                    if (!alive) continue;
+                    tc_fence_after();
+                    float v[HP];
+                    tmem_load<HP>(tS + set * 64 + lanes, v);
+                    tc_fence_before();
+                    mbar_arrive(&sfree[set]);
+                    const int j = i * 128 + lrow;
                     uint64_t acc = 0;   // even heads and odd heads
 #pragma unroll
                     for (int h = 0; h < HP; h += 4) {
@@ -413,76 +429,90 @@ __global__ void __launch_bounds__(kListTcThreads, 1)
                     float s0, s1;
                     unpack_f32x2(acc, s0, s1);
                     if (j < k) a.l.scores[(int64_t)t * k + j] = j < r.ncols ? (s0 + s1) + 0.f : -CUDART_INF_F;
-                } else {
-                    const float ej = j < r.ncols ? e : 0.f;
-                    if (j + 256 < r.ncols) e = a.l.ds[(int64_t)t * k + j + 256];
-                    // a place behind the list's end repeats the last key: its products count for nothing (e = 0)
-                    alive = tc_wait_warp(&gfree[set], ((g >> 1) & 1) ^ 1u, status, 32, abort_flag, alive);
-                    if (!alive) continue;
-                    uint8_t* grow = sG + set * SH::GTILE + lrow * 128;
-#pragma unroll
-                    for (int h0 = 0; h0 < HP; h0 += 8) {
-                        uint32_t p[4];
-#pragma unroll
-                        for (int h = 0; h < 8; h += 4) {
-                            const float4 w4 = *reinterpret_cast<const float4*>(w + h0 + h);
-                            const float wv[4] = {w4.x, w4.y, w4.z, w4.w};
-                            float gv[4];
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const float s = v[h0 + h + x];
-                                dw[h0 + h + x] = fmaf(ej, fmaxf(s, 0.f), dw[h0 + h + x]);
-                                gv[x] = s > 0.f ? ej * wv[x] : 0.f;
-                            }
-                            p[h / 2] = pack_bf16x2(gv[0], gv[1]);
-                            p[h / 2 + 1] = pack_bf16x2(gv[2], gv[3]);
-                        }
-                        *reinterpret_cast<uint4*>(grow + (((h0 / 8) ^ (lrow & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    mbar_arrive(&gfull[set]);
                 }
-            }
-            n += nt;
-            if constexpr (!BWD) {
-                // places behind the last tile (set 0's threads, which may still be a tile ahead or behind)
-                if (set == 0)
+                if (set == 0)   // places behind the last tile
                     for (int j = nt * 128 + st; j < k; j += 128) a.l.scores[(int64_t)t * k + j] = -CUDART_INF_F;
             } else {
-                warp_transpose_sum<HP>(dw, lane);
-                float* part = sDW + ((all & 1) * 8 + (warp - 2)) * HP;
-                if (lane < HP) part[lane] = dw[0];
-                if (HP == 64) part[lane + 32] = dw[32];
-                named_barrier(3, 256);
-                if (a.l.dW && set == 0 && st < H) {
-                    float s = 0.f;
+                constexpr int NC = HP / 4;     // heads (columns) of a set
+                const int c0 = set * NC;
+                float dw[NC];
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) s += sDW[((all & 1) * 8 + x) * HP + st];
-                    a.l.dW[(int64_t)t * H + st] = s;
+                for (int h = 0; h < NC; ++h) dw[h] = 0.f;
+                const float* ds = a.l.ds + (int64_t)t * k + lrow;
+                float e = lrow < r.ncols ? ds[0] : 0.f;
+                for (int i = 0; i < nt; ++i) {
+                    const int g = n + i, b = g & 1;
+                    alive = tc_wait_warp(&sfull[b], (g >> 1) & 1, status, 31, abort_flag, alive);
+                    if (!alive) continue;
+                    tc_fence_after();
+                    float v[NC];
+                    tmem_load<NC>(tS + b * 64 + c0 + lanes, v);
+                    tc_fence_before();
+                    mbar_arrive(&sfree[b]);
+                    // a place behind the list's end repeats the last key: its products count for nothing (e = 0)
+                    const int j = i * 128 + lrow;
+                    const float ej = j < r.ncols ? e : 0.f;
+                    if (j + 128 < r.ncols) e = ds[(i + 1) * 128];
+                    uint32_t p[NC / 2];
+#pragma unroll
+                    for (int h = 0; h < NC; h += 4) {
+                        const float4 w4 = *reinterpret_cast<const float4*>(w + c0 + h);
+                        const float wv[4] = {w4.x, w4.y, w4.z, w4.w};
+                        float gv[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const float s = v[h + x];
+                            dw[h + x] = fmaf(ej, fmaxf(s, 0.f), dw[h + x]);
+                            gv[x] = s > 0.f ? ej * wv[x] : 0.f;
+                        }
+                        p[h / 2] = pack_bf16x2(gv[0], gv[1]);
+                        p[h / 2 + 1] = pack_bf16x2(gv[2], gv[3]);
+                    }
+                    alive = tc_wait_warp(&gfree[b], ((g >> 1) & 1) ^ 1u, status, 32, abort_flag, alive);
+                    if (!alive) continue;
+                    uint8_t* grow = sG + b * SH::GTILE + lrow * 128;
+                    if constexpr (NC >= 8) {
+#pragma unroll
+                        for (int x = 0; x < NC / 8; ++x)
+                            *reinterpret_cast<uint4*>(grow + (((set * (NC / 8) + x) ^ (lrow & 7)) << 4)) =
+                                make_uint4(p[4 * x], p[4 * x + 1], p[4 * x + 2], p[4 * x + 3]);
+                    } else {
+                        *reinterpret_cast<uint2*>(grow + (((set / 2) ^ (lrow & 7)) << 4) + (set & 1) * 8) =
+                            make_uint2(p[0], p[1]);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    mbar_arrive(&gfull[b]);
                 }
-                constexpr int NC = HP == 16 ? 16 : HP / 2;   // columns (heads) a set writes
-                const int c0 = HP == 16 ? 0 : set * NC;
+                warp_transpose_sum<NC>(dw, lane);
+                float* part = sDW + (all & 1) * 4 * HP;
+                if (lane < NC) part[quarter * HP + c0 + lane] = dw[0];
+                named_barrier(5, 512);
+                const int h = threadIdx.x - 64;
+                if (a.l.dW && h < H)
+                    a.l.dW[(int64_t)t * H + h] = (part[h] + part[HP + h]) + (part[2 * HP + h] + part[3 * HP + h]);
                 if (nt > 0) {
                     const int qb = it & 1;
                     alive = tc_wait_warp(&dqfull[qb], (it >> 1) & 1, status, 33, abort_flag, alive);
                     if (alive) {
                         tc_fence_after();
                         float v[NC];
-                        if (HP > 16 || set == 0) tmem_load<NC>(tDQ + qb * 64 + c0 + lanes, v);
+                        tmem_load<NC>(tDQ + qb * 64 + c0 + lanes, v);
                         tc_fence_before();
                         mbar_arrive(&dqfree[qb]);
-                        if (a.l.dQ && lrow < D && (HP > 16 || set == 0)) {
+                        if (a.l.dQ && lrow < D) {
                             __nv_bfloat16* out = a.l.dQ + ((int64_t)t * H + c0) * D + lrow;
 #pragma unroll
                             for (int c = 0; c < NC; ++c)
                                 if (c0 + c < H) out[c * D] = __float2bfloat16_rn(v[c]);
                         }
+                        __syncwarp();
                     }
                 } else if (a.l.dQ) {   // nothing listed: zero gradients
-                    for (int o = threadIdx.x - 64; o < H * D; o += 256)
+                    for (int o = threadIdx.x - 64; o < H * D; o += 512)
                         a.l.dQ[(int64_t)t * H * D + o] = __float2bfloat16_rn(0.f);
                 }
             }
+            n += nt;
             if (nt > 0) ++it;
         }
     }

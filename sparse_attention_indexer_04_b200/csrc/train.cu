@@ -212,7 +212,7 @@ dsa_status list_tc_launch(const ListArgs& l, cudaStream_t st)
     dsa_status s = set_smem(list_tc_kernel<D, HP, BWD>, smem);
     if (s != DSA_OK) return s;
     DSA_LAUNCH(BWD ? kProfListDq : kProfListScores, st,
-               launch_pdl(true, list_tc_kernel<D, HP, BWD>, std::min(l.n_q, 148), kListTcThreads, smem, st, mq, a));
+               launch_pdl(true, list_tc_kernel<D, HP, BWD>, std::min(l.n_q, 148), list_threads(BWD), smem, st, mq, a));
     return launched();
 }
 
