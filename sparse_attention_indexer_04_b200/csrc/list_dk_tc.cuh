@@ -179,8 +179,8 @@ __global__ void __launch_bounds__(kDkThreads, 1)
         constexpr int CPR = D / 8, RPI = 32 / CPR, CPB = SH::ROWB / 16;
         const int chunk = lane % CPR, rsub = lane / CPR, cc = chunk % CPB;
         const uint32_t coff = (uint32_t)(chunk / CPB) * SH::QBOX;
-        // GL lanes per query of the block; a lane's first PF list places are read ahead
-        constexpr int GL = 32 / NQ, PF = 4;
+        // GL lanes per query of the block; a lane's list places are read PF at a time, the first ahead
+        constexpr int GL = 32 / NQ, PF = 8;
         const int q = lane / GL, sub = lane % GL;
         bool alive = true;
         struct Next {
@@ -204,15 +204,19 @@ __global__ void __launch_bounds__(kDkThreads, 1)
             const uint32_t ph = (uint32_t)((j / NS) & 1);
             const Next c = nx;
             // everything this block needs from memory is asked for before the first wait
-            const int64_t base = (int64_t)(q0 + c.t) * a.l.k;
+            const int32_t* lp = a.l.lists + (int64_t)(q0 + c.t) * a.l.k;
+            const float* dp = a.l.ds + (int64_t)(q0 + c.t) * a.l.k;
             int key[PF];
             float ds[PF];
+            auto read = [&](int i0) {
 #pragma unroll
-            for (int x = 0; x < PF; ++x) {
-                const int i = c.lo + sub + x * GL;
-                key[x] = i < c.hi ? a.l.lists[base + i] - s0 : -1;
-                ds[x] = i < c.hi ? a.l.ds[base + i] : 0.f;
-            }
+                for (int x = 0; x < PF; ++x) {
+                    const int i = i0 + x * GL;
+                    key[x] = i < c.hi ? __ldg(lp + i) : -1;
+                    ds[x] = i < c.hi ? __ldg(dp + i) : 0.f;
+                }
+            };
+            read(c.lo + sub);
             float wv[(ROWS + 31) / 32];
 #pragma unroll
             for (int x = 0; x < (ROWS + 31) / 32; ++x) {
@@ -243,13 +247,12 @@ __global__ void __launch_bounds__(kDkThreads, 1)
                 reinterpret_cast<float4*>(e)[x] = make_float4(0.f, 0.f, 0.f, 0.f);
             __syncwarp();
             e += q * kDkKeys;
+            for (int i = c.lo + sub;;) {
 #pragma unroll
-            for (int x = 0; x < PF; ++x)
-                if (key[x] >= 0 && DSA_CHECK(key[x] < kDkKeys, status, 115)) e[key[x]] = ds[x];
-#pragma unroll 4
-            for (int i = c.lo + sub + PF * GL; i < c.hi; i += GL) {
-                const int kk = a.l.lists[base + i] - s0;
-                if (DSA_CHECK(kk >= 0 && kk < kDkKeys, status, 115)) e[kk] = a.l.ds[base + i];
+                for (int x = 0; x < PF; ++x)
+                    if (key[x] >= 0 && DSA_CHECK(key[x] >= s0 && key[x] < s0 + kDkKeys, status, 115)) e[key[x] - s0] = ds[x];
+                if ((i += PF * GL) >= c.hi) break;
+                read(i);
             }
             __syncwarp();
             mbar_arrive(&efull[s]);
@@ -258,54 +261,70 @@ __global__ void __launch_bounds__(kDkThreads, 1)
         __syncwarp();
     } else if (warp == 4) {
         // -------------------------------------------------------- MMA issuer
-        if (lane == 0 && nb > 0) {   // (nothing listed: the epilogue writes zeros)
-            mbar_arrive_expect_tx(kfull, 2 * SH::KTILE);
-            for (int x = 0; x < 2; ++x)
-                for (int bx = 0; bx < SH::NBOX; ++bx)
-                    tma_load_2d(sK + x * SH::KTILE + bx * SH::KBOX, &tmK, bx * SH::BOXC, kb + s0 + x * 128, kfull);
+        if (nb > 0) {   // (nothing listed: the epilogue writes zeros)
+            if (elect_one()) {
+                mbar_arrive_expect_tx(kfull, 2 * SH::KTILE);
+                for (int x = 0; x < 2; ++x)
+                    for (int bx = 0; bx < SH::NBOX; ++bx)
+                        tma_load_2d(sK + x * SH::KTILE + bx * SH::KBOX, &tmK, bx * SH::BOXC, kb + s0 + x * 128, kfull);
+            }
+            __syncwarp();
             const uint32_t idS = idesc_bf16_f32(128, ROWS);
             const uint32_t idK = idesc_bf16_f32(128, D) | kIdescBMn;
-            bool alive = mbar_wait(kfull, 0, status, 43);
+            const uint64_t dKs = smem_desc_kmajor(smem_u32(sK), SH::ROWB), dQs = smem_desc_kmajor(smem_u32(sQ), SH::ROWB);
+            const uint64_t dG = smem_desc_kmajor(smem_u32(sG), 128);
+            const uint64_t dQt = smem_desc_mnmajor(smem_u32(sQ), SH::ROWB, SH::QBOX);
+            const uint32_t tbase = __shfl_sync(0xffffffffu, tmem, 0);
+            bool alive = __all_sync(0xffffffffu, mbar_wait(kfull, 0, status, 43));
             if (!alive) *abort_flag = 1;
             auto flush = [&](int j) {   // dK += G . Q of block j, both tiles
                 const int s = j % NS, b = j & 1;
-                for (int x = 0; x < 2 && alive; ++x) {
-                    alive = tc_wait(&gfull[x * 2 + b], (j >> 1) & 1, status, 44, abort_flag);
+                const uint64_t bd = dQt + s * (SH::QTILE >> 4);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    alive = tc_wait_warp(&gfull[x * 2 + b], (j >> 1) & 1, status, 44, abort_flag, alive);
                     if (!alive) return;
                     tc_fence_after();
+                    const uint64_t ad = dG + (x * 2 + b) * (SH::GTILE >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < ROWS / 16; ++kk) {
-                        const uint64_t ad = smem_desc_kmajor(smem_u32(sG + (x * 2 + b) * SH::GTILE) + kk * 32, 128);
-                        const uint64_t bd = smem_desc_mnmajor(
-                            smem_u32(sQ + s * SH::QTILE) + kk * 16 * SH::ROWB, SH::ROWB, SH::QBOX);
-                        tc_mma(tDK + x * D, ad, bd, idK, kk > 0 || j > 0 ? 1u : 0u);
+                        for (int kk = 0; kk < ROWS / 16; ++kk)
+                            tc_mma(tbase + x * D, ad + kk * 2, bd + kk * SH::ROWB, idK, kk > 0 || j > 0 ? 1u : 0u);
+                        tc_commit(&gfree[x * 2 + b]);
+                        if (x == 1) tc_commit(&qfree[s]);
                     }
-                    tc_commit(&gfree[x * 2 + b]);
+                    __syncwarp();
                 }
-                tc_commit(&qfree[s]);
             };
             for (int j = 0; j < nb && alive; ++j) {
                 const int s = j % NS, b = j & 1;
-                if (!(alive = tc_wait(&qfull[s], (j / NS) & 1, status, 45, abort_flag))) break;
+                alive = tc_wait_warp(&qfull[s], (j / NS) & 1, status, 45, abort_flag, alive);
+                if (!alive) break;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the copies, for the MMA's reads
-                for (int x = 0; x < 2 && alive; ++x) {
-                    alive = tc_wait(&sfree[x * 2 + b], ((j >> 1) & 1) ^ 1u, status, 46, abort_flag);
+                const uint64_t bd = dQs + s * (SH::QTILE >> 4);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    alive = tc_wait_warp(&sfree[x * 2 + b], ((j >> 1) & 1) ^ 1u, status, 46, abort_flag, alive);
                     if (!alive) break;
                     tc_fence_after();
+                    const uint64_t ad = dKs + x * (SH::KTILE >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const int bx = kk / (SH::BOXC / 16);
-                        const uint32_t ko = (kk % (SH::BOXC / 16)) * 32;
-                        const uint64_t ad = smem_desc_kmajor(smem_u32(sK + x * SH::KTILE + bx * SH::KBOX) + ko, SH::ROWB);
-                        const uint64_t bd = smem_desc_kmajor(smem_u32(sQ + s * SH::QTILE + bx * SH::QBOX) + ko, SH::ROWB);
-                        tc_mma(tS + (x * 2 + b) * 64, ad, bd, idS, kk > 0 ? 1u : 0u);
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const int bx = kk / (SH::BOXC / 16);
+                            const uint32_t ko = (kk % (SH::BOXC / 16)) * 2;
+                            tc_mma(tbase + 256 + (x * 2 + b) * 64, ad + bx * (SH::KBOX >> 4) + ko,
+                                   bd + bx * (SH::QBOX >> 4) + ko, idS, kk > 0 ? 1u : 0u);
+                        }
+                        tc_commit(&sfull[x * 2 + b]);
                     }
-                    tc_commit(&sfull[x * 2 + b]);
+                    __syncwarp();
                 }
                 if (j > 0 && alive) flush(j - 1);
             }
             if (alive) flush(nb - 1);
-            tc_commit(dkfull);   // every MMA issued so far
+            if (elect_one()) tc_commit(dkfull);   // every MMA issued so far
+            __syncwarp();
             mbar_wait(dkfull, 0, status, 47);
             if (!alive) mbar_wait(kfull, 0, status, 48);   // the key tiles have landed before the CTA leaves
         }

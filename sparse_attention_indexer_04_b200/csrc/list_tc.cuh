@@ -104,6 +104,16 @@ __device__ __forceinline__ bool tc_wait_warp(uint64_t* bar, uint32_t parity, uin
     return __all_sync(0xffffffffu, alive && tc_wait(bar, parity, status, where, abort_flag));
 }
 
+// True in one lane of the warp, the same one every time.  The issuing warp runs its loops whole and
+// only the MMAs and commits under this, so that descriptors stay in uniform registers: built by a
+// single diverged lane they cost about 150 clocks an MMA.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t on;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+    return on != 0;
+}
+
 __device__ __forceinline__ void named_barrier(int id, int threads)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -308,82 +318,85 @@ __global__ void __launch_bounds__(list_threads(BWD), 1)
         __syncwarp();
     } else if (warp == 1) {
         // -------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            const uint32_t idS = idesc_bf16_f32(128, HP);
-            const uint32_t idQ = idesc_bf16_f32(128, HP) | kIdescAMn | kIdescBMn;
-            int stage = 0;
-            uint32_t phase = 0;
-            int n = 0, it = 0;     // tiles and non-empty queries so far
-            // the product of the tile before, issued after the next tile's S so that the two overlap
-            bool pend = false, pend_first = false, pend_last = false;
-            int pend_stage = 0, pend_it = 0, pend_n = 0;
-            bool alive = true;
-            auto flush = [&]() {
-                if (!pend || !alive) return;
-                pend = false;
-                const int b = pend_n & 1, qb = pend_it & 1;
-                if (!tc_wait(&gfull[b], (pend_n >> 1) & 1, status, 25, abort_flag)) { alive = false; return; }
-                if (pend_first && !tc_wait(&dqfree[qb], ((pend_it >> 1) & 1) ^ 1u, status, 26, abort_flag)) {
-                    alive = false;
-                    return;
-                }
-                tc_fence_after();
+        const uint32_t idS = idesc_bf16_f32(128, HP);
+        const uint32_t idQ = idesc_bf16_f32(128, HP) | kIdescAMn | kIdescBMn;
+        // operands at stage 0 / buffer 0; the address field counts 16-byte units
+        const uint64_t dKs = smem_desc_kmajor(smem_u32(sK), SH::ROWB), dQs = smem_desc_kmajor(smem_u32(sQ), SH::ROWB);
+        const uint64_t dKt = smem_desc_mnmajor(smem_u32(sK), SH::ROWB, SH::KBOX);
+        const uint64_t dGt = smem_desc_mnmajor(smem_u32(sG), 128, 0);
+        const uint32_t tbase = __shfl_sync(0xffffffffu, tmem, 0);
+        int stage = 0;
+        uint32_t phase = 0;
+        int n = 0, it = 0;     // tiles and non-empty queries so far
+        // the product of the tile before, issued after the next tile's S so that the two overlap
+        bool pend = false, pend_first = false, pend_last = false;
+        int pend_stage = 0, pend_it = 0, pend_n = 0;
+        bool alive = true;
+        auto flush = [&]() {
+            if (!pend || !alive) return;
+            pend = false;
+            const int b = pend_n & 1, qb = pend_it & 1;
+            alive = tc_wait_warp(&gfull[b], (pend_n >> 1) & 1, status, 25, abort_flag, alive);
+            if (pend_first) alive = tc_wait_warp(&dqfree[qb], ((pend_it >> 1) & 1) ^ 1u, status, 26, abort_flag, alive);
+            if (!alive) return;
+            tc_fence_after();
+            const uint64_t ad = dKt + pend_stage * (SH::KTILE >> 4), bd = dGt + b * (SH::GTILE >> 4);
+            if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {   // 16 keys each
-                    const uint64_t ad = smem_desc_mnmajor(
-                        smem_u32(sK + pend_stage * SH::KTILE) + kk * 16 * SH::ROWB, SH::ROWB, SH::KBOX);
-                    const uint64_t bd = smem_desc_mnmajor(smem_u32(sG + b * SH::GTILE) + kk * 16 * 128, 128, 0);
-                    tc_mma(tDQ + qb * 64, ad, bd, idQ, kk > 0 || !pend_first ? 1u : 0u);
-                }
+                for (int kk = 0; kk < 8; ++kk)   // 16 keys each
+                    tc_mma(tbase + 128 + qb * 64, ad + kk * (SH::ROWB), bd + kk * 128, idQ,
+                           kk > 0 || !pend_first ? 1u : 0u);
                 tc_commit(&kempty[pend_stage]);
                 tc_commit(&gfree[b]);
                 if (pend_last) tc_commit(&dqfull[qb]);
-            };
-            RowDesc nx = (int)blockIdx.x < n_q ? a.l.rows[blockIdx.x] : none;
-            for (int t = blockIdx.x; t < n_q && alive; t += step) {
-                const RowDesc r = nx;
-                if (t + step < n_q) nx = a.l.rows[t + step];
-                const int nt = (r.ncols + 127) >> 7;
-                if (nt == 0) continue;
-                const int qb = it & 1;
-                if (!tc_wait(&qfull[qb], (it >> 1) & 1, status, 27, abort_flag)) break;
-                for (int i = 0; i < nt && alive; ++i, ++n) {
-                    const int b = n & 1;
-                    if (!tc_wait(&full[stage], phase, status, 28, abort_flag)) { alive = false; break; }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the copies, for the MMA's reads
-                    if (!tc_wait(&sfree[b], ((n >> 1) & 1) ^ 1u, status, 29, abort_flag)) { alive = false; break; }
-                    tc_fence_after();
+            }
+            __syncwarp();
+        };
+        int nx = (int)blockIdx.x < n_q ? a.l.rows[blockIdx.x].ncols : 0;
+        for (int t = blockIdx.x; t < n_q && alive; t += step) {
+            const int nt = __shfl_sync(0xffffffffu, (nx + 127) >> 7, 0);
+            if (t + step < n_q) nx = a.l.rows[t + step].ncols;
+            if (nt == 0) continue;
+            const int qb = it & 1;
+            alive = tc_wait_warp(&qfull[qb], (it >> 1) & 1, status, 27, abort_flag, alive);
+            for (int i = 0; i < nt && alive; ++i, ++n) {
+                const int b = n & 1;
+                alive = tc_wait_warp(&full[stage], phase, status, 28, abort_flag, alive);
+                alive = tc_wait_warp(&sfree[b], ((n >> 1) & 1) ^ 1u, status, 29, abort_flag, alive);
+                if (!alive) break;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the copies, for the MMA's reads
+                tc_fence_after();
+                const uint64_t ad = dKs + stage * (SH::KTILE >> 4), bd = dQs + qb * (SH::QTILE >> 4);
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const int bx = kk / (SH::BOXC / 16);
-                        const uint32_t ko = (kk % (SH::BOXC / 16)) * 32;
-                        const uint64_t ad =
-                            smem_desc_kmajor(smem_u32(sK + stage * SH::KTILE + bx * SH::KBOX) + ko, SH::ROWB);
-                        const uint64_t bd =
-                            smem_desc_kmajor(smem_u32(sQ + qb * SH::QTILE + bx * SH::QBOX) + ko, SH::ROWB);
-                        tc_mma(tS + b * 64, ad, bd, idS, kk > 0 ? 1u : 0u);
+                        const uint32_t ko = (kk % (SH::BOXC / 16)) * 2;   // 16 values of a row: 32 bytes
+                        tc_mma(tbase + b * 64, ad + bx * (SH::KBOX >> 4) + ko, bd + bx * (SH::QBOX >> 4) + ko, idS,
+                               kk > 0 ? 1u : 0u);
                     }
                     tc_commit(&sfull[b]);
                     if (i == nt - 1) tc_commit(&qempty[qb]);
-                    if constexpr (BWD) {
-                        flush();
-                        pend = true;
-                        pend_first = i == 0;
-                        pend_last = i == nt - 1;
-                        pend_stage = stage;
-                        pend_it = it;
-                        pend_n = n;
-                    } else {
-                        tc_commit(&kempty[stage]);
-                    }
-                    if (++stage == n_stages) { stage = 0; phase ^= 1u; }
+                    if (!BWD) tc_commit(&kempty[stage]);
                 }
-                ++it;
+                __syncwarp();
+                if constexpr (BWD) {
+                    flush();
+                    pend = true;
+                    pend_first = i == 0;
+                    pend_last = i == nt - 1;
+                    pend_stage = stage;
+                    pend_it = it;
+                    pend_n = n;
+                }
+                if (++stage == n_stages) { stage = 0; phase ^= 1u; }
             }
-            if constexpr (BWD) flush();
-            tc_commit(drain);   // every MMA issued has completed before TMEM is released
-            mbar_wait(drain, 0, status, 30);
+            ++it;
         }
+        if constexpr (BWD) flush();
+        if (elect_one()) tc_commit(drain);   // every MMA issued has completed before TMEM is released
+        __syncwarp();
+        mbar_wait(drain, 0, status, 30);
         __syncwarp();
     } else {
         // ---------------------------------------------------------- epilogue
