@@ -5,8 +5,10 @@
 // tiles of 128, resident in shared memory, their dK accumulators in TMEM for the CTA's whole life)
 // and passes over the queries that list any of them, NQ = up to 64 / H at a time:
 //   S[128 keys x ROWS] = K_tile . Q^T      (ROWS = NQ * H query-head rows)
-//   G = S > 0 ? ds w : 0                    (bf16, shared memory; ds scattered from the list's places)
-//   dK_tile += G . Q                        (A = G K-major, B = Q MN-major as it lies)
+//   G = S > 0 ? ds w : 0                    (bf16, in TMEM over S; ds scattered from the list's places)
+//   dK_tile += G . Q                        (A = G from TMEM, B = Q MN-major as it lies)
+// (G in shared memory had the products read 8 KB an MMA there, which its bandwidth, not the tensor
+// cores, paced: 92 clocks an MMA of 64.)
 // No atomics and no scatter of rows: each (key tile, query) product is dense, keys that the query does
 // not list have G = 0.  That does up to 1 / density of the needed work, but the alternative, a
 // 512-byte fp32 row added to memory per listed pair, costs more until lists cover less than about
@@ -52,18 +54,20 @@ struct DkShape {
     static constexpr uint32_t KTILE = KBOX * NBOX;
     static constexpr uint32_t QBOX = (uint32_t)ROWS * ROWB;
     static constexpr uint32_t QTILE = QBOX * NBOX;
-    static constexpr uint32_t GTILE = 128u * 128u;
-    static constexpr int NS = NQ >= 8 ? 3 : 4;                     // stages of queries
+    static constexpr int NS = 4;                                   // stages of queries
+    // TMEM columns of G inside its S buffer: a set's half of the rows, packed in pairs, over the S
+    // columns it has read itself; 16 rows are one MMA's k and need adjacent columns (free ones of the slot)
+    static constexpr int g_half(int half) { return ROWS == 16 ? 32 + half * 4 : half * (ROWS / 2); }
+    static constexpr int g_step(int kk) { return ROWS == 64 ? (kk / 2) * 32 + (kk % 2) * 8 : ROWS == 32 ? kk * 16 : 32; }
     static constexpr uint32_t E_BYTES = (uint32_t)NQ * kDkKeys * 4;
     static constexpr uint32_t q_off = 2 * KTILE;
-    static constexpr uint32_t g_off = q_off + NS * QTILE;          // [tile][parity]
-    static constexpr uint32_t e_off = g_off + 4 * GTILE;
+    static constexpr uint32_t e_off = q_off + NS * QTILE;
     static constexpr uint32_t w_off = e_off + NS * E_BYTES;
     static constexpr uint32_t list_off = w_off + NS * 64 * 4;
     static constexpr uint32_t bar_off = list_off + kDkMaxList * 2;
     static constexpr uint32_t bytes = bar_off + 512;
     static_assert(NS <= 4 && ROWS % (32 / (D / 8)) == 0);
-    static_assert(g_off % 1024 == 0 && q_off % 1024 == 0 && bytes <= 232448, "shared memory of the dK kernel");
+    static_assert(q_off % 1024 == 0 && bytes <= 232448, "shared memory of the dK kernel");
 };
 
 struct DkArgs {
@@ -106,7 +110,6 @@ __global__ void __launch_bounds__(kDkThreads, 1)
 
     uint8_t* sK = smem;
     uint8_t* sQ = smem + SH::q_off;
-    uint8_t* sG = smem + SH::g_off;
     float* sE = reinterpret_cast<float*>(smem + SH::e_off);
     float* sW = reinterpret_cast<float*>(smem + SH::w_off);
     uint16_t* sList = reinterpret_cast<uint16_t*>(smem + SH::list_off);
@@ -118,8 +121,7 @@ __global__ void __launch_bounds__(kDkThreads, 1)
     uint64_t* sfull = efree + NS;         // [tile][parity]
     uint64_t* sfree = sfull + 4;
     uint64_t* gfull = sfree + 4;
-    uint64_t* gfree = gfull + 4;
-    uint64_t* dkfull = gfree + 4;
+    uint64_t* dkfull = gfull + 4;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dkfull + 1);
     volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
     int32_t* sCount = reinterpret_cast<int32_t*>(tmem_slot + 2);   // [21] per-warp counts
@@ -135,9 +137,8 @@ __global__ void __launch_bounds__(kDkThreads, 1)
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&sfull[i], 1);
-            mbar_init(&sfree[i], 256);
+            mbar_init(&sfree[i], 1);
             mbar_init(&gfull[i], 256);
-            mbar_init(&gfree[i], 1);
         }
         mbar_init(dkfull, 1);
         *abort_flag = 0;
@@ -272,7 +273,6 @@ __global__ void __launch_bounds__(kDkThreads, 1)
             const uint32_t idS = idesc_bf16_f32(128, ROWS);
             const uint32_t idK = idesc_bf16_f32(128, D) | kIdescBMn;
             const uint64_t dKs = smem_desc_kmajor(smem_u32(sK), SH::ROWB), dQs = smem_desc_kmajor(smem_u32(sQ), SH::ROWB);
-            const uint64_t dG = smem_desc_kmajor(smem_u32(sG), 128);
             const uint64_t dQt = smem_desc_mnmajor(smem_u32(sQ), SH::ROWB, SH::QBOX);
             const uint32_t tbase = __shfl_sync(0xffffffffu, tmem, 0);
             bool alive = __all_sync(0xffffffffu, mbar_wait(kfull, 0, status, 43));
@@ -285,12 +285,12 @@ __global__ void __launch_bounds__(kDkThreads, 1)
                     alive = tc_wait_warp(&gfull[x * 2 + b], (j >> 1) & 1, status, 44, abort_flag, alive);
                     if (!alive) return;
                     tc_fence_after();
-                    const uint64_t ad = dG + (x * 2 + b) * (SH::GTILE >> 4);
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < ROWS / 16; ++kk)
-                            tc_mma(tbase + x * D, ad + kk * 2, bd + kk * SH::ROWB, idK, kk > 0 || j > 0 ? 1u : 0u);
-                        tc_commit(&gfree[x * 2 + b]);
+                            tc_mma_ta(tbase + x * D, tbase + 256 + (x * 2 + b) * 64 + SH::g_step(kk), bd + kk * SH::ROWB,
+                                      idK, kk > 0 || j > 0 ? 1u : 0u);
+                        tc_commit(&sfree[x * 2 + b]);
                         if (x == 1) tc_commit(&qfree[s]);
                     }
                     __syncwarp();
@@ -349,8 +349,6 @@ __global__ void __launch_bounds__(kDkThreads, 1)
             tc_fence_after();
             float v[NC];
             tmem_load<NC>(tS + sb * 64 + c0 + lanes, v);
-            tc_fence_before();
-            mbar_arrive(&sfree[sb]);
             const float* w = sW + s * 64 + c0;
             uint32_t g[NC / 2];
 #pragma unroll
@@ -363,14 +361,8 @@ __global__ void __launch_bounds__(kDkThreads, 1)
                 g[c / 2 + 1] = pack_bf16x2(v[c + 2], v[c + 3]);
             }
             mbar_arrive(&efree[s]);
-            alive = tc_wait_warp(&gfree[sb], ((j >> 1) & 1) ^ 1u, status, 51, abort_flag, alive);
-            if (!alive) break;
-            uint8_t* grow = sG + sb * SH::GTILE + lrow * 128;
-#pragma unroll
-            for (int c = 0; c < NC / 8; ++c)
-                *reinterpret_cast<uint4*>(grow + (((half * (NC / 8) + c) ^ (lrow & 7)) << 4)) =
-                    make_uint4(g[4 * c], g[4 * c + 1], g[4 * c + 2], g[4 * c + 3]);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            tmem_store<NC / 2>(tS + sb * 64 + SH::g_half(half) + lanes, g);
+            tc_fence_before();
             mbar_arrive(&gfull[sb]);
         }
         // the finished rows
