@@ -3,7 +3,7 @@
 //
 // The sum runs over queries, so the keys stay: a CTA owns 256 consecutive keys of a sequence (two
 // tiles of 128, resident in shared memory, their dK accumulators in TMEM for the CTA's whole life)
-// and passes over the queries that list any of them, NQ = up to 64 / H at a time:
+// and passes over the queries that list any of them, NQ = up to 128 / H at a time:
 //   S[128 keys x ROWS] = K_tile . Q^T      (ROWS = NQ * H query-head rows)
 //   G = S > 0 ? ds w : 0                    (bf16, in TMEM over S; ds scattered from the list's places)
 //   dK_tile += G . Q                        (A = G from TMEM, B = Q MN-major as it lies)
@@ -45,8 +45,9 @@ __global__ void list_edges_kernel(const int32_t* lists, int32_t k, const RowDesc
 
 template <int D, int H>
 struct DkShape {
-    static constexpr int NQ = H >= 8 ? 64 / H : H >= 2 ? 8 : 16;   // queries of a block
-    static constexpr int ROWS = NQ * H;                            // 16, 32 or 64
+    static constexpr int NQ = H >= 8 ? 128 / H : 16;               // queries of a block
+    static constexpr int ROWS = NQ * H;                            // 16, 32, 64 or 128
+    static constexpr int CW = ROWS >= 64 ? 32 : ROWS / 2;          // columns of S a thread takes at a time
     static constexpr uint32_t ROWB = D * 2 >= 128 ? 128 : 64;
     static constexpr int BOXC = ROWB / 2;
     static constexpr int NBOX = D / BOXC;
@@ -54,19 +55,19 @@ struct DkShape {
     static constexpr uint32_t KTILE = KBOX * NBOX;
     static constexpr uint32_t QBOX = (uint32_t)ROWS * ROWB;
     static constexpr uint32_t QTILE = QBOX * NBOX;
-    static constexpr int NS = 4;                                   // stages of queries
-    // TMEM columns of G inside its S buffer: a set's half of the rows, packed in pairs, over the S
-    // columns it has read itself; 16 rows are one MMA's k and need adjacent columns (free ones of the slot)
-    static constexpr int g_half(int half) { return ROWS == 16 ? 32 + half * 4 : half * (ROWS / 2); }
-    static constexpr int g_step(int kk) { return ROWS == 64 ? (kk / 2) * 32 + (kk % 2) * 8 : ROWS == 32 ? kk * 16 : 32; }
+    static constexpr int NS = 3;                                   // stages of queries
+    // TMEM columns of G inside the tile's S: CW values packed in pairs over S columns that the same
+    // threads have read; 16 rows are one MMA's k and need adjacent columns (free ones)
+    static constexpr int g_chunk(int c0) { return ROWS == 16 ? 32 + c0 / 2 : c0; }
+    static constexpr int g_step(int kk) { return ROWS >= 64 ? (kk / 2) * 32 + (kk % 2) * 8 : ROWS == 32 ? kk * 16 : 32; }
     static constexpr uint32_t E_BYTES = (uint32_t)NQ * kDkKeys * 4;
     static constexpr uint32_t q_off = 2 * KTILE;
     static constexpr uint32_t e_off = q_off + NS * QTILE;
     static constexpr uint32_t w_off = e_off + NS * E_BYTES;
-    static constexpr uint32_t list_off = w_off + NS * 64 * 4;
+    static constexpr uint32_t list_off = w_off + NS * ROWS * 4;
     static constexpr uint32_t bar_off = list_off + kDkMaxList * 2;
     static constexpr uint32_t bytes = bar_off + 512;
-    static_assert(NS <= 4 && ROWS % (32 / (D / 8)) == 0);
+    static_assert(NS <= 4 && list_off % 8 == 0 && ROWS % (32 / (D / 8)) == 0);
     static_assert(q_off % 1024 == 0 && bytes <= 232448, "shared memory of the dK kernel");
 };
 
@@ -118,10 +119,10 @@ __global__ void __launch_bounds__(kDkThreads, 1)
     uint64_t* qfree = qfull + NS;         // [NS] both products have read them
     uint64_t* efull = qfree + NS;         // [NS] ds and weights are written
     uint64_t* efree = efull + NS;         // [NS] and read
-    uint64_t* sfull = efree + NS;         // [tile][parity]
-    uint64_t* sfree = sfull + 4;
-    uint64_t* gfull = sfree + 4;
-    uint64_t* dkfull = gfull + 4;
+    uint64_t* sfull = efree + NS;         // [tile] S is complete
+    uint64_t* sfree = sfull + 2;          // [tile] G, which lies over S, has been read
+    uint64_t* gfull = sfree + 2;          // [tile] G is written
+    uint64_t* dkfull = gfull + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dkfull + 1);
     volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
     int32_t* sCount = reinterpret_cast<int32_t*>(tmem_slot + 2);   // [21] per-warp counts
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kDkThreads, 1)
             mbar_init(&efull[i], 32);
             mbar_init(&efree[i], 512);
         }
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 1);
             mbar_init(&sfree[i], 1);
             mbar_init(&gfull[i], 256);
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kDkThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t tDK = tmem, tS = tmem + 256;   // dK: tile * D; S: (tile * 2 + parity) * 64
+    const uint32_t tDK = tmem, tS = tmem + 256;   // dK: tile * D; S: tile * 128
 
     if (warp < 4) {
         // -------------------------------------------------------- loaders
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(kDkThreads, 1)
             cp_async_arrive(&qfull[s]);
             alive = tc_wait_warp(&efree[s], ph ^ 1u, status, 42, abort_flag, alive);
             if (!alive) break;
-            float* w = sW + s * 64;
+            float* w = sW + s * ROWS;
 #pragma unroll
             for (int x = 0; x < (ROWS + 31) / 32; ++x)
                 if (x * 32 + lane < ROWS) w[x * 32 + lane] = wv[x];
@@ -277,34 +278,33 @@ __global__ void __launch_bounds__(kDkThreads, 1)
             const uint32_t tbase = __shfl_sync(0xffffffffu, tmem, 0);
             bool alive = __all_sync(0xffffffffu, mbar_wait(kfull, 0, status, 43));
             if (!alive) *abort_flag = 1;
-            auto flush = [&](int j) {   // dK += G . Q of block j, both tiles
-                const int s = j % NS, b = j & 1;
+            auto flush = [&](int j, int x) {   // dK += G . Q of block j, tile x
+                const int s = j % NS;
                 const uint64_t bd = dQt + s * (SH::QTILE >> 4);
+                alive = tc_wait_warp(&gfull[x], j & 1, status, 44, abort_flag, alive);
+                if (!alive) return;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    alive = tc_wait_warp(&gfull[x * 2 + b], (j >> 1) & 1, status, 44, abort_flag, alive);
-                    if (!alive) return;
-                    tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < ROWS / 16; ++kk)
-                            tc_mma_ta(tbase + x * D, tbase + 256 + (x * 2 + b) * 64 + SH::g_step(kk), bd + kk * SH::ROWB,
-                                      idK, kk > 0 || j > 0 ? 1u : 0u);
-                        tc_commit(&sfree[x * 2 + b]);
-                        if (x == 1) tc_commit(&qfree[s]);
-                    }
-                    __syncwarp();
+                    for (int kk = 0; kk < ROWS / 16; ++kk)
+                        tc_mma_ta(tbase + x * D, tbase + 256 + x * 128 + SH::g_step(kk), bd + kk * SH::ROWB, idK,
+                                  kk > 0 || j > 0 ? 1u : 0u);
+                    tc_commit(&sfree[x]);
+                    if (x == 1) tc_commit(&qfree[s]);
                 }
+                __syncwarp();
             };
+            // the two tiles take turns: one's S, then the other's dK, so that a tile's epilogue runs
+            // beside the other tile's products
             for (int j = 0; j < nb && alive; ++j) {
-                const int s = j % NS, b = j & 1;
+                const int s = j % NS;
                 alive = tc_wait_warp(&qfull[s], (j / NS) & 1, status, 45, abort_flag, alive);
                 if (!alive) break;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the copies, for the MMA's reads
                 const uint64_t bd = dQs + s * (SH::QTILE >> 4);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    alive = tc_wait_warp(&sfree[x * 2 + b], ((j >> 1) & 1) ^ 1u, status, 46, abort_flag, alive);
+                    alive = tc_wait_warp(&sfree[x], (j & 1) ^ 1u, status, 46, abort_flag, alive);
                     if (!alive) break;
                     tc_fence_after();
                     const uint64_t ad = dKs + x * (SH::KTILE >> 4);
@@ -313,16 +313,17 @@ __global__ void __launch_bounds__(kDkThreads, 1)
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const int bx = kk / (SH::BOXC / 16);
                             const uint32_t ko = (kk % (SH::BOXC / 16)) * 2;
-                            tc_mma(tbase + 256 + (x * 2 + b) * 64, ad + bx * (SH::KBOX >> 4) + ko,
-                                   bd + bx * (SH::QBOX >> 4) + ko, idS, kk > 0 ? 1u : 0u);
+                            tc_mma(tbase + 256 + x * 128, ad + bx * (SH::KBOX >> 4) + ko, bd + bx * (SH::QBOX >> 4) + ko,
+                                   idS, kk > 0 ? 1u : 0u);
                         }
-                        tc_commit(&sfull[x * 2 + b]);
+                        tc_commit(&sfull[x]);
                     }
                     __syncwarp();
+                    if (x == 1) flush(j, 0);
+                    else if (j > 0) flush(j - 1, 1);
                 }
-                if (j > 0 && alive) flush(j - 1);
             }
-            if (alive) flush(nb - 1);
+            if (alive) flush(nb - 1, 1);
             if (elect_one()) tc_commit(dkfull);   // every MMA issued so far
             __syncwarp();
             mbar_wait(dkfull, 0, status, 47);
@@ -334,36 +335,39 @@ __global__ void __launch_bounds__(kDkThreads, 1)
         const int quarter = warp & 3, set = (warp - 5) >> 3, half = ((warp - 5) >> 2) & 1;
         const int lrow = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        constexpr int NC = ROWS / 2;   // query-head rows (columns of S) of a set
-        const int c0 = half * NC;
+        constexpr int CW = SH::CW;
         bool alive = true;
         for (int j = 0; j < nb; ++j) {
-            const int s = j % NS, b = j & 1, sb = set * 2 + b;
+            const int s = j % NS;
             alive = tc_wait_warp(&efull[s], (j / NS) & 1, status, 49, abort_flag, alive);
-            const float* e = sE + (s * NQ + (NQ > 1 ? half * (NQ / 2) : 0)) * kDkKeys + set * 128 + lrow;
-            float eq[NQ > 1 ? NQ / 2 : 1];
-#pragma unroll
-            for (int q = 0; q < (NQ > 1 ? NQ / 2 : 1); ++q) eq[q] = alive ? e[q * kDkKeys] : 0.f;
-            alive = tc_wait_warp(&sfull[sb], (j >> 1) & 1, status, 50, abort_flag, alive);
+            alive = tc_wait_warp(&sfull[set], j & 1, status, 50, abort_flag, alive);
             if (!alive) break;
             tc_fence_after();
-            float v[NC];
-            tmem_load<NC>(tS + sb * 64 + c0 + lanes, v);
-            const float* w = sW + s * 64 + c0;
-            uint32_t g[NC / 2];
+            const float* e = sE + s * NQ * kDkKeys + set * 128 + lrow;
 #pragma unroll
-            for (int c = 0; c < NC; c += 4) {
-                const float4 w4 = *reinterpret_cast<const float4*>(w + c);
-                const float wv[4] = {w4.x, w4.y, w4.z, w4.w};
+            for (int x = 0; x < ROWS / 2; x += CW) {
+                const int c0 = half * (ROWS / 2) + x;   // query-head rows (columns of S) c0 .. c0 + CW - 1
+                float v[CW];
+                tmem_load<CW>(tS + set * 128 + c0 + lanes, v);
+                const float* w = sW + s * ROWS + c0;
+                float eq[CW > H ? CW / H : 1];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) v[c + x] = v[c + x] > 0.f ? eq[NQ > 1 ? (c + x) / H : 0] * wv[x] : 0.f;
-                g[c / 2] = pack_bf16x2(v[c], v[c + 1]);
-                g[c / 2 + 1] = pack_bf16x2(v[c + 2], v[c + 3]);
+                for (int q = 0; q < (CW > H ? CW / H : 1); ++q) eq[q] = e[(c0 / H + q) * kDkKeys];
+                uint32_t g[CW / 2];
+#pragma unroll
+                for (int c = 0; c < CW; c += 4) {
+                    const float4 w4 = *reinterpret_cast<const float4*>(w + c);
+                    const float wv[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) v[c + y] = v[c + y] > 0.f ? eq[CW > H ? (c + y) / H : 0] * wv[y] : 0.f;
+                    g[c / 2] = pack_bf16x2(v[c], v[c + 1]);
+                    g[c / 2 + 1] = pack_bf16x2(v[c + 2], v[c + 3]);
+                }
+                tmem_store<CW / 2>(tS + set * 128 + SH::g_chunk(c0) + lanes, g);
             }
-            mbar_arrive(&efree[s]);
-            tmem_store<NC / 2>(tS + sb * 64 + SH::g_half(half) + lanes, g);
             tc_fence_before();
-            mbar_arrive(&gfull[sb]);
+            mbar_arrive(&gfull[set]);
+            mbar_arrive(&efree[s]);
         }
         // the finished rows
         if (nb > 0) {
