@@ -10,8 +10,8 @@
 //     dW_h = sum_j e max(0, S[j,h])                       (fp32 registers, joined once per query)
 // The tile is read once for both products, so a query moves its listed keys from L2 exactly once;
 // that gather (256 bytes per listed pair at d = 128) is what bounds the kernel, not the products.
-// Roles: warp 0 and the last three gather; warp 1 issues the MMAs; the warps between them are the
-// epilogue.  S is double-buffered, so a tile's product runs while the tile before is worked on.
+// Roles: warp 0 and three late ones gather; warp 1 issues S, the last warp dQ; the warps between are
+// the epilogue.  S is double-buffered, so a tile's product runs while the tile before is worked on.
 // HP = max(16, H): heads above H have zero rows in the query tile.  Every wait is bounded.
 #pragma once
 
@@ -22,12 +22,12 @@
 
 namespace dsa {
 
-// Epilogue warps: forward two sets of four on alternate tiles; backward four sets of four on each tile,
-// a quarter of the heads each (one set a tile left the kernel bound by the latency of a tile's epilogue
-// at 2600 clocks, 64 heads a thread).
+// Epilogue warps: two groups on alternate tiles, of four warps (forward) or of eight (backward: two sets,
+// half of the heads each).  Measured backward, 4096 queries x 2048 keys, H = 64: 64 heads a thread in two
+// groups 556 us, 16 heads a thread in one group 322 us (both with one issuer's other steps alike).
 constexpr int kListTcProducers = 4;
 constexpr int list_sets(bool bwd) { return bwd ? 4 : 2; }
-constexpr int list_threads(bool bwd) { return 32 * (1 + kListTcProducers) + 128 * list_sets(bwd); }
+constexpr int list_threads(bool bwd) { return 32 * (1 + kListTcProducers + (bwd ? 1 : 0)) + 128 * list_sets(bwd); }
 constexpr uint32_t kErrListAlign = 3;
 
 // Shared-memory matrix descriptor of an MN-major operand: rows of the K dimension are row_bytes
@@ -185,7 +185,7 @@ struct ListShape {
     static constexpr uint32_t QTILE = QBOX * NBOX;
     static constexpr uint32_t GTILE = 128u * 128u;   // rows of 128 bytes, the first HP heads used
     static constexpr uint32_t W_BYTES = 4u * 2u * HP * 4;         // [set][parity][head]
-    static constexpr uint32_t DW_BYTES = 2u * 4u * HP * 4;        // [parity][warp of the set][head]
+    static constexpr uint32_t DW_BYTES = 2u * 8u * HP * 4;        // [parity][group][quarter][head]
     static constexpr uint32_t BAR_BYTES = 512;
     static constexpr uint32_t align1k(uint32_t x) { return (x + 1023u) & ~1023u; }
     // key stages, query tiles, G tiles, then the small arrays.  An operand tile narrower than the
@@ -201,7 +201,26 @@ struct ListTcArgs {
     int32_t n_stages;
 };
 
-// Sums N (at most 16) per-lane values over the warp: lane i < N ends with the sum of value i in v[0].
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// The bf16 pair (e w where s > 0, else 0) of two products s: 0 - s has its sign bit set exactly where
+// s > 0 (zeros of either sign give +0), and that bit, spread over 16 bits, masks the rounded e w.
+__device__ __forceinline__ uint32_t relu_grad_pair(float s0, float s1, uint64_t ee, uint64_t ww)
+{
+    float n0, n1, g0, g1;
+    unpack_f32x2(fma_f32x2(pack_f32x2(s0, s1), pack_f32x2(-1.f, -1.f), 0), n0, n1);
+    unpack_f32x2(mul_f32x2(ee, ww), g0, g1);
+    uint32_t m;   // bytes 0, 1: the sign of n0 eight times over; 2, 3: of n1
+    asm("prmt.b32 %0, %1, %2, 0xFFBB;" : "=r"(m) : "r"(__float_as_uint(n0)), "r"(__float_as_uint(n1)));
+    return pack_bf16x2(g0, g1) & m;
+}
+
+// Sums N (at most 32) per-lane values over the warp: lane i < N ends with the sum of value i in v[0].
 // Each step halves the number of values, so N values cost about N shuffles.
 template <int N>
 __device__ __forceinline__ void warp_transpose_sum(float* v, int lane)
@@ -247,8 +266,8 @@ __global__ void __launch_bounds__(list_threads(BWD), 1)
     uint64_t* gfree = gfull + 2;               // [2] G has been read
     uint64_t* dqfull = gfree + 2;              // [2] dQ of a query is complete
     uint64_t* dqfree = dqfull + 2;             // [2] dQ has been read
-    uint64_t* drain = dqfree + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* drain = dqfree + 2;              // [2] one per issuing warp
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
     volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
 
     constexpr int kEpi = 4 * list_sets(BWD);   // epilogue warps 2 .. kEpi + 1
@@ -260,13 +279,13 @@ __global__ void __launch_bounds__(list_threads(BWD), 1)
             mbar_init(&qfull[i], 1);
             mbar_init(&qempty[i], 1);
             mbar_init(&sfull[i], 1);
-            mbar_init(&sfree[i], BWD ? 512 : 128);
-            mbar_init(&gfull[i], 512);
+            mbar_init(&sfree[i], BWD ? 256 : 128);
+            mbar_init(&gfull[i], 256);
             mbar_init(&gfree[i], 1);
             mbar_init(&dqfull[i], 1);
             mbar_init(&dqfree[i], 512);
         }
-        mbar_init(drain, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);
         *abort_flag = 0;
         fence_barrier_init();
         prefetch_tensormap(&tmQ);
@@ -285,7 +304,7 @@ __global__ void __launch_bounds__(list_threads(BWD), 1)
     const int n_q = a.l.n_q, H = a.l.H, k = a.l.k, step = gridDim.x;
     const RowDesc none{0, 0, 0, 0};
 
-    if (warp == 0 || warp >= 2 + kEpi) {
+    if (warp == 0 || (warp >= 2 + kEpi && warp < 5 + kEpi)) {
         // ------------------------------------------------------ producers
         // Four warps of 32 tile rows each, 16 bytes a lane (asynchronous copies, two rows of 256 bytes
         // an instruction at d = 128).  Gathering the same tile with TMA (gather4) took 2400 clocks.
@@ -353,41 +372,15 @@ __global__ void __launch_bounds__(list_threads(BWD), 1)
             }
         __syncwarp();
     } else if (warp == 1) {
-        // -------------------------------------------------------- MMA issuer
+        // -------------------------------------------------------- S issuer
         const uint32_t idS = idesc_bf16_f32(128, HP);
-        const uint32_t idQ = idesc_bf16_f32(128, HP) | kIdescAMn | kIdescBMn;
         // operands at stage 0 / buffer 0; the address field counts 16-byte units
         const uint64_t dKs = smem_desc_kmajor(smem_u32(sK), SH::ROWB), dQs = smem_desc_kmajor(smem_u32(sQ), SH::ROWB);
-        const uint64_t dKt = smem_desc_mnmajor(smem_u32(sK), SH::ROWB, SH::KBOX);
-        const uint64_t dGt = smem_desc_mnmajor(smem_u32(sG), 128, 0);
         const uint32_t tbase = __shfl_sync(0xffffffffu, tmem, 0);
         int stage = 0;
         uint32_t phase = 0;
         int n = 0, it = 0;     // tiles and non-empty queries so far
-        // the product of the tile before, issued after the next tile's S so that the two overlap
-        bool pend = false, pend_first = false, pend_last = false;
-        int pend_stage = 0, pend_it = 0, pend_n = 0;
         bool alive = true;
-        auto flush = [&]() {
-            if (!pend || !alive) return;
-            pend = false;
-            const int b = pend_n & 1, qb = pend_it & 1;
-            alive = tc_wait_warp(&gfull[b], (pend_n >> 1) & 1, status, 25, abort_flag, alive);
-            if (pend_first) alive = tc_wait_warp(&dqfree[qb], ((pend_it >> 1) & 1) ^ 1u, status, 26, abort_flag, alive);
-            if (!alive) return;
-            tc_fence_after();
-            const uint64_t ad = dKt + pend_stage * (SH::KTILE >> 4), bd = dGt + b * (SH::GTILE >> 4);
-            if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)   // 16 keys each
-                    tc_mma(tbase + 128 + qb * 64, ad + kk * (SH::ROWB), bd + kk * 128, idQ,
-                           kk > 0 || !pend_first ? 1u : 0u);
-                tc_commit(&kempty[pend_stage]);
-                tc_commit(&gfree[b]);
-                if (pend_last) tc_commit(&dqfull[qb]);
-            }
-            __syncwarp();
-        };
         int nx = (int)blockIdx.x < n_q ? a.l.rows[blockIdx.x].ncols : 0;
         for (int t = blockIdx.x; t < n_q && alive; t += step) {
             const int nt = __shfl_sync(0xffffffffu, (nx + 127) >> 7, 0);
@@ -416,23 +409,55 @@ __global__ void __launch_bounds__(list_threads(BWD), 1)
                     if (!BWD) tc_commit(&kempty[stage]);
                 }
                 __syncwarp();
-                if constexpr (BWD) {
-                    flush();
-                    pend = true;
-                    pend_first = i == 0;
-                    pend_last = i == nt - 1;
-                    pend_stage = stage;
-                    pend_it = it;
-                    pend_n = n;
-                }
                 if (++stage == n_stages) { stage = 0; phase ^= 1u; }
             }
             ++it;
         }
-        if constexpr (BWD) flush();
-        if (elect_one()) tc_commit(drain);   // every MMA issued has completed before TMEM is released
+        if (elect_one()) tc_commit(&drain[0]);   // every MMA issued has completed before TMEM is released
         __syncwarp();
-        mbar_wait(drain, 0, status, 30);
+        mbar_wait(&drain[0], 0, status, 30);
+        __syncwarp();
+    } else if (BWD && warp == 5 + kEpi) {
+        // -------------------------------------------------------- dQ issuer
+        // A warp of its own: its waits and the S issuer's overlap (one issuer left the tensor cores
+        // idle for about 550 clocks a tile).
+        const uint32_t idQ = idesc_bf16_f32(128, HP) | kIdescAMn | kIdescBMn;
+        const uint64_t dKt = smem_desc_mnmajor(smem_u32(sK), SH::ROWB, SH::KBOX);
+        const uint64_t dGt = smem_desc_mnmajor(smem_u32(sG), 128, 0);
+        const uint32_t tbase = __shfl_sync(0xffffffffu, tmem, 0) + 128;
+        int stage = 0, n = 0, it = 0;
+        bool alive = true;
+        int nx = (int)blockIdx.x < n_q ? a.l.rows[blockIdx.x].ncols : 0;
+        for (int t = blockIdx.x; t < n_q && alive; t += step) {
+            const int nt = __shfl_sync(0xffffffffu, (nx + 127) >> 7, 0);
+            if (t + step < n_q) nx = a.l.rows[t + step].ncols;
+            if (nt == 0) continue;
+            const int qb = it & 1;
+            alive = tc_wait_warp(&dqfree[qb], ((it >> 1) & 1) ^ 1u, status, 26, abort_flag, alive);
+            for (int i = 0; i < nt && alive; ++i, ++n) {
+                const int b = n & 1;
+                // (G is written from this tile's S: the tile has landed, and the S issuer saw it)
+                alive = tc_wait_warp(&gfull[b], (n >> 1) & 1, status, 25, abort_flag, alive);
+                if (!alive) break;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                tc_fence_after();
+                const uint64_t ad = dKt + stage * (SH::KTILE >> 4), bd = dGt + b * (SH::GTILE >> 4);
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)   // 16 keys each
+                        tc_mma(tbase + qb * 64, ad + kk * SH::ROWB, bd + kk * 128, idQ, kk > 0 || i > 0 ? 1u : 0u);
+                    tc_commit(&kempty[stage]);
+                    tc_commit(&gfree[b]);
+                    if (i == nt - 1) tc_commit(&dqfull[qb]);
+                }
+                __syncwarp();
+                if (++stage == n_stages) stage = 0;
+            }
+            ++it;
+        }
+        if (elect_one()) tc_commit(&drain[1]);
+        __syncwarp();
+        mbar_wait(&drain[1], 0, status, 34);
         __syncwarp();
     } else {
         // ---------------------------------------------------------- epilogue
@@ -482,77 +507,82 @@ __global__ void __launch_bounds__(list_threads(BWD), 1)
                 if (set == 0)   // places behind the last tile
                     for (int j = nt * 128 + st; j < k; j += 128) a.l.scores[(int64_t)t * k + j] = -CUDART_INF_F;
             } else {
-                constexpr int NC = HP / 4;     // heads (columns) of a set
-                const int c0 = set * NC;
-                float dw[NC];
+                constexpr int NC = HP / 2;     // heads (columns) of a set
+                const int grp = set >> 1, half = set & 1, c0 = half * NC;
+                uint64_t dw[NC / 2];           // pairs of heads
 #pragma unroll
-                for (int h = 0; h < NC; ++h) dw[h] = 0.f;
+                for (int h = 0; h < NC / 2; ++h) dw[h] = 0;
                 const float* ds = a.l.ds + (int64_t)t * k + lrow;
-                float e = lrow < r.ncols ? ds[0] : 0.f;
-                for (int i = 0; i < nt; ++i) {
-                    const int g = n + i, b = g & 1;
-                    alive = tc_wait_warp(&sfull[b], (g >> 1) & 1, status, 31, abort_flag, alive);
+                int i = (n & 1) == grp ? 0 : 1;   // the group's first tile
+                float e = i * 128 + lrow < r.ncols ? ds[i * 128] : 0.f;
+                for (; i < nt; i += 2) {
+                    const uint32_t use = (uint32_t)((n + i) >> 1) & 1u;
+                    // a place behind the list's end repeats the last key: its products count for nothing (e = 0)
+                    const uint64_t ee = pack_f32x2(e, e);
+                    e = (i + 2) * 128 + lrow < r.ncols ? ds[(i + 2) * 128] : 0.f;
+                    alive = tc_wait_warp(&sfull[grp], use, status, 31, abort_flag, alive);
+                    alive = tc_wait_warp(&gfree[grp], use ^ 1u, status, 32, abort_flag, alive);
                     if (!alive) continue;
                     tc_fence_after();
-                    float v[NC];
-                    tmem_load<NC>(tS + b * 64 + c0 + lanes, v);
-                    tc_fence_before();
-                    mbar_arrive(&sfree[b]);
-                    // a place behind the list's end repeats the last key: its products count for nothing (e = 0)
-                    const int j = i * 128 + lrow;
-                    const float ej = j < r.ncols ? e : 0.f;
-                    if (j + 128 < r.ncols) e = ds[(i + 1) * 128];
-                    uint32_t p[NC / 2];
+                    uint8_t* grow = sG + grp * SH::GTILE + lrow * 128;
+                    constexpr int CW = NC < 16 ? NC : 16;   // columns in registers at once
+                    float v[CW];
 #pragma unroll
-                    for (int h = 0; h < NC; h += 4) {
-                        const float4 w4 = *reinterpret_cast<const float4*>(w + c0 + h);
-                        const float wv[4] = {w4.x, w4.y, w4.z, w4.w};
-                        float gv[4];
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const float s = v[h + x];
-                            dw[h + x] = fmaf(ej, fmaxf(s, 0.f), dw[h + x]);
-                            gv[x] = s > 0.f ? ej * wv[x] : 0.f;
+                    for (int h = 0; h < NC; h += 8) {
+                        if (h % CW == 0) {
+                            tmem_load<CW>(tS + grp * 64 + c0 + h + lanes, v);
+                            if (h + CW == NC) {
+                                tc_fence_before();
+                                mbar_arrive(&sfree[grp]);
+                            }
                         }
-                        p[h / 2] = pack_bf16x2(gv[0], gv[1]);
-                        p[h / 2 + 1] = pack_bf16x2(gv[2], gv[3]);
-                    }
-                    alive = tc_wait_warp(&gfree[b], ((g >> 1) & 1) ^ 1u, status, 32, abort_flag, alive);
-                    if (!alive) continue;
-                    uint8_t* grow = sG + b * SH::GTILE + lrow * 128;
-                    if constexpr (NC >= 8) {
+                        uint32_t p[4];
 #pragma unroll
-                        for (int x = 0; x < NC / 8; ++x)
-                            *reinterpret_cast<uint4*>(grow + (((set * (NC / 8) + x) ^ (lrow & 7)) << 4)) =
-                                make_uint4(p[4 * x], p[4 * x + 1], p[4 * x + 2], p[4 * x + 3]);
-                    } else {
-                        *reinterpret_cast<uint2*>(grow + (((set / 2) ^ (lrow & 7)) << 4) + (set & 1) * 8) =
-                            make_uint2(p[0], p[1]);
+                        for (int x = 0; x < 8; x += 4) {
+                            const ulonglong2 w2 = *reinterpret_cast<const ulonglong2*>(w + c0 + h + x);
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const float s0 = v[h % CW + x + 2 * y], s1 = v[h % CW + x + 2 * y + 1];
+                                uint64_t& acc = dw[(h + x) / 2 + y];
+                                acc = fma_f32x2(ee, pack_f32x2(fmaxf(s0, 0.f), fmaxf(s1, 0.f)), acc);
+                                p[x / 2 + y] = relu_grad_pair(s0, s1, ee, y ? w2.y : w2.x);
+                            }
+                        }
+                        *reinterpret_cast<uint4*>(grow + (((c0 + h) / 8 ^ (lrow & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    mbar_arrive(&gfull[b]);
+                    mbar_arrive(&gfull[grp]);
                 }
-                warp_transpose_sum<NC>(dw, lane);
-                float* part = sDW + (all & 1) * 4 * HP;
-                if (lane < NC) part[quarter * HP + c0 + lane] = dw[0];
+                float dv[NC];
+#pragma unroll
+                for (int h = 0; h < NC / 2; ++h) unpack_f32x2(dw[h], dv[2 * h], dv[2 * h + 1]);
+                warp_transpose_sum<NC>(dv, lane);
+                float* part = sDW + (all & 1) * 8 * HP;
+                if (lane < NC) part[(grp * 4 + quarter) * HP + c0 + lane] = dv[0];
                 named_barrier(5, 512);
                 const int h = threadIdx.x - 64;
-                if (a.l.dW && h < H)
-                    a.l.dW[(int64_t)t * H + h] = (part[h] + part[HP + h]) + (part[2 * HP + h] + part[3 * HP + h]);
+                if (a.l.dW && h < H) {
+                    float s = 0.f;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) s += part[x * HP + h];
+                    a.l.dW[(int64_t)t * H + h] = s;
+                }
+                constexpr int NR = HP / 4;     // heads whose dQ a set writes
+                const int r0 = set * NR;
                 if (nt > 0) {
                     const int qb = it & 1;
                     alive = tc_wait_warp(&dqfull[qb], (it >> 1) & 1, status, 33, abort_flag, alive);
                     if (alive) {
                         tc_fence_after();
-                        float v[NC];
-                        tmem_load<NC>(tDQ + qb * 64 + c0 + lanes, v);
+                        float v[NR];
+                        tmem_load<NR>(tDQ + qb * 64 + r0 + lanes, v);
                         tc_fence_before();
                         mbar_arrive(&dqfree[qb]);
                         if (a.l.dQ && lrow < D) {
-                            __nv_bfloat16* out = a.l.dQ + ((int64_t)t * H + c0) * D + lrow;
+                            __nv_bfloat16* out = a.l.dQ + ((int64_t)t * H + r0) * D + lrow;
 #pragma unroll
-                            for (int c = 0; c < NC; ++c)
-                                if (c0 + c < H) out[c * D] = __float2bfloat16_rn(v[c]);
+                            for (int c = 0; c < NR; ++c)
+                                if (r0 + c < H) out[c * D] = __float2bfloat16_rn(v[c]);
                         }
                         __syncwarp();
                     }
