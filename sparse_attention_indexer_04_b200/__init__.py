@@ -362,38 +362,59 @@ def hisa_index(layout: Layout, Q, K, W, pooled, k: int, block: int, keep: int, i
 # ---------------------------------------------------------------- training
 
 _TYPES = {torch.bfloat16: BF16, torch.float32: FP32}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _rows(t, name, device, shape=None, dtype=None):
-    """A 2-D row matrix the library can read in place: unit stride along a row, on `device`."""
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name}: expected a 2-D tensor{'' if shape is None else f' of shape {shape}'}, "
-                         f"got {tuple(t.shape)}")
+def _rows(t, name, index, n=None, d=None, dtype=None):
+    """Row stride of a 2-D matrix that the library can read in place: adjacent values along a row, on the
+    CUDA device `index`."""
+    shape = t.shape
+    if len(shape) != 2 or (n is not None and (shape[0] != n or shape[1] != d)):
+        raise ValueError(f"{name}: expected a 2-D tensor{'' if n is None else f' of shape {(n, d)}'}, "
+                         f"got {tuple(shape)}")
     if t.dtype not in _TYPES if dtype is None else t.dtype != dtype:
         raise ValueError(f"{name}: {t.dtype} is not supported here")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    ld, unit = t.stride()
+    if shape[1] > 1 and unit != 1:
         raise ValueError(f"{name}: values of a row must be adjacent")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    if shape[0] <= 1:
+        return shape[1]
+    if ld < shape[1]:
         raise ValueError(f"{name}: rows overlap")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return ld
 
 
-def _dense(t, name, device, shape, dtype):
-    """A contiguous tensor of the given shape and type on `device`; None passes."""
+def _dense(t, name, index, shape, dtype):
+    """Address of a contiguous tensor of the given shape and type on the CUDA device `index`; None passes."""
     if t is None:
-        return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+        return None
+    if t.shape != shape or t.dtype != dtype or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
 def _device(t):
-    """The CUDA device of a tensor, with an index (the library has no CPU path)."""
+    """The CUDA device index of a tensor (the library has no CPU path)."""
     if not t.is_cuda:
         raise ValueError("expected CUDA tensors")
-    return t.device
+    return t.get_device()
+
+
+def _on(index, call, *args, stream=None):
+    """call(*args, stream) with the CUDA device `index` current; stream: that device's current one by default."""
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _on(index, call, *args, stream=stream)
+    if stream is not None:
+        raw = stream.cuda_stream
+    elif _raw_stream is not None:
+        raw = _raw_stream(index)
+    else:
+        raw = torch.cuda.current_stream(index).cuda_stream
+    return call(*args, raw)
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, out_dtype=None, want_stats=False, stream=None):
@@ -402,18 +423,16 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, out_dtype
     dev = _device(x)
     ld_x = _rows(x, "x", dev)
     n, d = x.shape
-    _dense(weight, "weight", dev, (d,), torch.float32)
-    _dense(bias, "bias", dev, (d,), torch.float32)
-    with torch.cuda.device(dev):
-        if out is None:
-            out = torch.empty(n, d, dtype=out_dtype or x.dtype, device=dev)
-        ld_y = _rows(out, "out", dev, (n, d))
-        mean = rstd = None
-        if want_stats:
-            mean, rstd = torch.empty(2, n, dtype=torch.float32, device=dev).unbind(0)
-        _check(_lib.dsa_layer_norm(n, d, _ptr(x), _TYPES[x.dtype], ld_x, _ptr(weight), _ptr(bias), eps, _ptr(out),
-                                   _TYPES[out.dtype], ld_y, _ptr(mean), _ptr(rstd), _stream(stream)),
-               "dsa_layer_norm")
+    w, b = _dense(weight, "weight", dev, (d,), torch.float32), _dense(bias, "bias", dev, (d,), torch.float32)
+    if out is None:
+        out = torch.empty((n, d), dtype=out_dtype or x.dtype, device=x.device)
+    ld_y = _rows(out, "out", dev, n, d)
+    mean = rstd = mp = rp = None
+    if want_stats:
+        mean, rstd = x.new_empty(n, dtype=torch.float32), x.new_empty(n, dtype=torch.float32)
+        mp, rp = mean.data_ptr(), rstd.data_ptr()
+    _check(_on(dev, _lib.dsa_layer_norm, n, d, x.data_ptr(), _TYPES[x.dtype], ld_x, w, b, eps, out.data_ptr(),
+               _TYPES[out.dtype], ld_y, mp, rp, stream=stream), "dsa_layer_norm")
     return (out, mean, rstd) if want_stats else out
 
 
@@ -426,19 +445,17 @@ def layer_norm_backward(dy, x, weight, mean, rstd, dx=None, ws=None, stream=None
     dev = _device(x)
     ld_x = _rows(x, "x", dev)
     n, d = x.shape
-    ld_dy = _rows(dy, "dy", dev, (n, d))
-    _dense(weight, "weight", dev, (d,), torch.float32)
-    _dense(mean, "mean", dev, (n,), torch.float32)
-    _dense(rstd, "rstd", dev, (n,), torch.float32)
-    with torch.cuda.device(dev):
-        if dx is None:
-            dx = torch.empty(n, d, dtype=x.dtype, device=dev)
-        ld_dx = _rows(dx, "dx", dev, (n, d), x.dtype)
-        dw, db = torch.empty(2, d, dtype=torch.float32, device=dev).unbind(0)
-        ws = _workspace(layer_norm_backward_workspace(n, d), dev, ws)
-        _check(_lib.dsa_layer_norm_backward(n, d, _ptr(dy), _TYPES[dy.dtype], ld_dy, _ptr(x), _TYPES[x.dtype], ld_x,
-                                            _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx), ld_dx, _ptr(dw), _ptr(db),
-                                            _ptr(ws), _bytes(ws), _stream(stream)), "dsa_layer_norm_backward")
+    ld_dy = _rows(dy, "dy", dev, n, d)
+    w = _dense(weight, "weight", dev, (d,), torch.float32)
+    mp, rp = _dense(mean, "mean", dev, (n,), torch.float32), _dense(rstd, "rstd", dev, (n,), torch.float32)
+    if dx is None:
+        dx = x.new_empty((n, d))
+    ld_dx = _rows(dx, "dx", dev, n, d, x.dtype)
+    dw, db = x.new_empty(d, dtype=torch.float32), x.new_empty(d, dtype=torch.float32)
+    ws = _workspace(layer_norm_backward_workspace(n, d), x.device, ws)
+    _check(_on(dev, _lib.dsa_layer_norm_backward, n, d, dy.data_ptr(), _TYPES[dy.dtype], ld_dy, x.data_ptr(),
+               _TYPES[x.dtype], ld_x, w, mp, rp, dx.data_ptr(), ld_dx, dw.data_ptr(), db.data_ptr(), ws.data_ptr(),
+               ws.numel() * ws.element_size(), stream=stream), "dsa_layer_norm_backward")
     return dx, dw, db
 
 
@@ -450,34 +467,33 @@ def distill_topk(scores, teacher, lists=None, kind: int = TEACHER_LOGITS, temper
     dev = _device(scores)
     ld_s = _rows(scores, "scores", dev, dtype=torch.float32)
     n, k = scores.shape
-    ld_t = _rows(teacher, "teacher", dev, (n, k))
-    ld_l = 0 if lists is None else _rows(lists, "lists", dev, (n, k), torch.int32)
-    _dense(grad_loss, "grad_loss", dev, (n,), torch.float32)
-    with torch.cuda.device(dev):
-        if loss is None:
-            loss = torch.empty(n, dtype=torch.float32, device=dev)
-        if dscores is None:
-            dscores = torch.empty(n, k, dtype=torch.float32, device=dev)
-        _dense(loss, "loss", dev, (n,), torch.float32)
-        ld_d = _rows(dscores, "dscores", dev, (n, k), torch.float32)
-        _check(_lib.dsa_distill_topk(n, k, _ptr(scores), ld_s, _ptr(lists), ld_l, _ptr(teacher), _TYPES[teacher.dtype],
-                                     ld_t, kind, temperature, _ptr(grad_loss), _ptr(loss), _ptr(dscores), ld_d,
-                                     _stream(stream)), "dsa_distill_topk")
+    ld_t = _rows(teacher, "teacher", dev, n, k)
+    lp, ld_l = (None, 0) if lists is None else (lists.data_ptr(), _rows(lists, "lists", dev, n, k, torch.int32))
+    g = _dense(grad_loss, "grad_loss", dev, (n,), torch.float32)
+    if loss is None:
+        loss = scores.new_empty(n)
+    if dscores is None:
+        dscores = scores.new_empty((n, k))
+    ld_d = _rows(dscores, "dscores", dev, n, k, torch.float32)
+    _check(_on(dev, _lib.dsa_distill_topk, n, k, scores.data_ptr(), ld_s, lp, ld_l, teacher.data_ptr(),
+               _TYPES[teacher.dtype], ld_t, kind, temperature, g, _dense(loss, "loss", dev, (n,), torch.float32),
+               dscores.data_ptr(), ld_d, stream=stream), "dsa_distill_topk")
     return loss, dscores
 
 
 def _list_inputs(layout, Q, K, W, lists):
+    """Device index, list length, and the addresses of Q, K, W and lists."""
     dev = _device(Q)
-    H, d, n_q, n_k = layout.num_heads, layout.head_dim, layout.num_queries, layout.c.num_keys
-    if layout.q_off.device != dev:
-        raise ValueError(f"Q is on {dev}, the layout on {layout.q_off.device}")
-    _dense(Q, "Q", dev, (n_q, H, d), torch.bfloat16)
-    _dense(K, "K", dev, (n_k, d), torch.bfloat16)
-    _dense(W, "W", dev, (n_q, H), torch.float32)
+    c = layout.c
+    H, d, n_q = c.num_heads, c.head_dim, c.num_queries
+    if layout.q_off.get_device() != dev:
+        raise ValueError(f"Q is on {Q.device}, the layout on {layout.q_off.device}")
     if lists.dim() != 2:
         raise ValueError("lists: expected [n_q, k]")
-    _dense(lists, "lists", dev, (n_q, lists.shape[1]), torch.int32)
-    return dev, n_q, int(lists.shape[1])
+    k = lists.shape[1]
+    return (dev, k, _dense(Q, "Q", dev, (n_q, H, d), torch.bfloat16),
+            _dense(K, "K", dev, (c.num_keys, d), torch.bfloat16), _dense(W, "W", dev, (n_q, H), torch.float32),
+            _dense(lists, "lists", dev, (n_q, k), torch.int32))
 
 
 def list_scores_workspace(layout: Layout, k: int) -> int:
@@ -487,15 +503,14 @@ def list_scores_workspace(layout: Layout, k: int) -> int:
 def list_scores(layout: Layout, Q, K, W, lists, scores=None, ws=None, stream=None):
     """Indexer scores at listed keys: lists [n_q, k] int32 (ascending, -1 padded) -> scores [n_q, k] fp32, -inf
     where a place is empty or its key is not in the query's prefix."""
-    dev, n_q, k = _list_inputs(layout, Q, K, W, lists)
-    with torch.cuda.device(dev):
-        if scores is None:
-            scores = torch.empty(n_q, k, dtype=torch.float32, device=dev)
-        _dense(scores, "scores", dev, (n_q, k), torch.float32)
-        ws = _workspace(list_scores_workspace(layout, k), dev, ws)
-        _check(_lib.dsa_list_scores(layout.ref(), _ptr(Q), _ptr(K), _ptr(W), k, _ptr(lists), _ptr(scores), _ptr(ws),
-                                    _bytes(ws), _stream(stream)), "dsa_list_scores")
-        _after(ws, "dsa_list_scores", stream)
+    dev, k, q, kk, w, l = _list_inputs(layout, Q, K, W, lists)
+    if scores is None:
+        scores = W.new_empty(lists.shape)
+    ws = _workspace(list_scores_workspace(layout, k), Q.device, ws)
+    _check(_on(dev, _lib.dsa_list_scores, layout.ref(), q, kk, w, k, l,
+               _dense(scores, "scores", dev, lists.shape, torch.float32), ws.data_ptr(), ws.numel() * ws.element_size(),
+               stream=stream), "dsa_list_scores")
+    _after(ws, "dsa_list_scores", stream)
     return scores
 
 
@@ -505,20 +520,17 @@ def list_scores_backward_workspace(layout: Layout, k: int) -> int:
 
 def list_scores_backward(layout: Layout, Q, K, W, lists, dscores, dQ=None, dK=None, dW=None, ws=None, stream=None):
     """Backward pass of list_scores: (dQ [n_q, H, d] bf16, dK [n_k, d] bf16, dW [n_q, H] fp32)."""
-    dev, n_q, k = _list_inputs(layout, Q, K, W, lists)
-    _dense(dscores, "dscores", dev, (n_q, k), torch.float32)
-    with torch.cuda.device(dev):
-        dQ = torch.empty_like(Q) if dQ is None else dQ
-        dK = torch.empty_like(K) if dK is None else dK
-        dW = torch.empty_like(W) if dW is None else dW
-        _dense(dQ, "dQ", dev, Q.shape, torch.bfloat16)
-        _dense(dK, "dK", dev, K.shape, torch.bfloat16)
-        _dense(dW, "dW", dev, W.shape, torch.float32)
-        ws = _workspace(list_scores_backward_workspace(layout, k), dev, ws)
-        _check(_lib.dsa_list_scores_backward(layout.ref(), _ptr(Q), _ptr(K), _ptr(W), k, _ptr(lists), _ptr(dscores),
-                                             _ptr(dQ), _ptr(dK), _ptr(dW), _ptr(ws), _bytes(ws), _stream(stream)),
-               "dsa_list_scores_backward")
-        _after(ws, "dsa_list_scores_backward", stream)
+    dev, k, q, kk, w, l = _list_inputs(layout, Q, K, W, lists)
+    ds = _dense(dscores, "dscores", dev, lists.shape, torch.float32)
+    dQ = torch.empty_like(Q) if dQ is None else dQ
+    dK = torch.empty_like(K) if dK is None else dK
+    dW = torch.empty_like(W) if dW is None else dW
+    ws = _workspace(list_scores_backward_workspace(layout, k), Q.device, ws)
+    _check(_on(dev, _lib.dsa_list_scores_backward, layout.ref(), q, kk, w, k, l, ds,
+               _dense(dQ, "dQ", dev, Q.shape, torch.bfloat16), _dense(dK, "dK", dev, K.shape, torch.bfloat16),
+               _dense(dW, "dW", dev, W.shape, torch.float32), ws.data_ptr(), ws.numel() * ws.element_size(),
+               stream=stream), "dsa_list_scores_backward")
+    _after(ws, "dsa_list_scores_backward", stream)
     return dQ, dK, dW
 
 
