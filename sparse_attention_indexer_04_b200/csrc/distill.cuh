@@ -9,8 +9,10 @@
 // logarithm c_j (c_j = (t_j - max t) / tau, f = e^c; or f = t, c = log t) and y = sum f:
 //   loss = (sum f (c - a)) / y + log z - log y,
 // so two joint reductions over the row (the maxima, then z, y and the cross sum) give everything.
-// Bound by memory: a row is read once into registers and its gradient written once.  Rows longer
-// than the registers of a CTA hold (kDistillRegCols) are swept three times, the later sweeps from L2.
+// Bound by memory: a row is read once into registers and its gradient written once.  Exponentials
+// are base 2, one multiply and one instruction each (with expf and logf the arithmetic took as long
+// as the memory: 61.6 us for 8192 x 2048).  Rows longer than the registers of a CTA hold
+// (kDistillRegCols) are swept twice, the second time mostly from L2.
 #pragma once
 
 #include <math_constants.h>
@@ -19,7 +21,7 @@
 
 namespace dsa {
 
-constexpr int kDistillRegCols = 16384;
+constexpr int kDistillRegCols = 20480;   // 1024 threads x 20 places, two values each in 64 registers
 
 struct DistillArgs {
     const float* s;
@@ -35,40 +37,31 @@ struct DistillArgs {
     int32_t n, k;
     int32_t weights;       // the teacher's values: 0 logits, 1 weights
     float inv_tau;
+    float scale;           // log2(e) / tau: exponents are taken to base 2
+    int32_t off0, off_step; // VEC 4: row r starts (off0 + r * off_step) % 4 places behind a 4-place boundary
 };
 
-template <int VEC>
-__device__ __forceinline__ void distill_load(const float* p, float* v)
+// Places c .. c + VEC - 1 of a row of k (VEC 4: p + c on a 4-element boundary); with EDGE places outside
+// the row are not touched, else there are none.
+template <int VEC, bool EDGE, typename X, typename V>
+__device__ __forceinline__ void distill_load(const X* p, int c, int k, V* v)
 {
-    if constexpr (VEC == 4) {
-        const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    } else {
-        v[0] = __ldcs(p);
+    if (VEC == 4 && (!EDGE || (c >= 0 && c + 3 < k))) {
+        if constexpr (sizeof(X) == 2) {
+            const uint2 a = __ldcs(reinterpret_cast<const uint2*>(p + c));
+            v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xffff0000u);
+            v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xffff0000u);
+        } else if constexpr (sizeof(V) == sizeof(int32_t) && V(0.5f) == V(0)) {
+            const int4 a = __ldcs(reinterpret_cast<const int4*>(p + c));
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        } else {
+            const float4 a = __ldcs(reinterpret_cast<const float4*>(p + c));
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        }
+        return;
     }
-}
-
-template <int VEC>
-__device__ __forceinline__ void distill_load(const __nv_bfloat16* p, float* v)
-{
-    if constexpr (VEC == 4) {
-        const uint2 a = __ldcs(reinterpret_cast<const uint2*>(p));
-        v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xffff0000u);
-        v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xffff0000u);
-    } else {
-        v[0] = __bfloat162float(*p);
-    }
-}
-
-template <int VEC>
-__device__ __forceinline__ void distill_load(const int32_t* p, int32_t* v)
-{
-    if constexpr (VEC == 4) {
-        const int4 a = __ldcs(reinterpret_cast<const int4*>(p));
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    } else {
-        v[0] = __ldcs(p);
-    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = !EDGE || (c + e >= 0 && c + e < k) ? (V)p[c + e] : V(0);
 }
 
 // Joint reductions over the T threads of a row: a warp's lanes (T = 32) or the whole CTA.
@@ -81,12 +74,16 @@ __device__ __forceinline__ void distill_max2(float& a, float& b, float4* red)
         b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
     }
     if constexpr (T > 32) {
+        constexpr int NW = T / 32;
         if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float4(a, b, 0.f, 0.f);
         __syncthreads();
+        const float4 v = red[threadIdx.x & (NW - 1)];
+        a = v.x;
+        b = v.y;
 #pragma unroll
-        for (int i = 0; i < T / 32; ++i) {
-            a = fmaxf(a, red[i].x);
-            b = fmaxf(b, red[i].y);
+        for (int o = NW / 2; o > 0; o >>= 1) {
+            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
         }
     }
 }
@@ -101,28 +98,46 @@ __device__ __forceinline__ void distill_sum3(float& a, float& b, float& c, float
         c += __shfl_xor_sync(0xffffffffu, c, o);
     }
     if constexpr (T > 32) {
+        constexpr int NW = T / 32;
         if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float4(a, b, c, 0.f);
         __syncthreads();
-        a = b = c = 0.f;
+        const float4 v = red[threadIdx.x & (NW - 1)];
+        a = v.x;
+        b = v.y;
+        c = v.z;
 #pragma unroll
-        for (int i = 0; i < T / 32; ++i) {
-            const float4 v = red[i];
-            a += v.x;
-            b += v.y;
-            c += v.z;
+        for (int o = NW / 2; o > 0; o >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            b += __shfl_xor_sync(0xffffffffu, b, o);
+            c += __shfl_xor_sync(0xffffffffu, c, o);
         }
     }
 }
 
-// The teacher's unnormalised weight of a counted place and the logarithm that goes with it.
+// 2^x to about 2 units in the last place, log2 x to 2^-22 absolute around 1.
+__device__ __forceinline__ float distill_exp2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float distill_log2(float x)
+{
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The teacher's unnormalised weight of a counted place and its base-2 logarithm c.
 __device__ __forceinline__ float distill_weight(float t, float mt, const DistillArgs& a, float& c)
 {
     if (a.weights) {
-        c = logf(t);
+        c = distill_log2(t);
         return t;
     }
-    c = (t - mt) * a.inv_tau;
-    return expf(c);
+    c = (t - mt) * a.scale;
+    return distill_exp2(c);
 }
 
 // What a row's sums say: the loss, and the factors of e^a and f in the gradient.
@@ -134,14 +149,14 @@ __device__ __forceinline__ DistillRow distill_row(float z, float y, float x, flo
 {
     DistillRow r{0.f, 0.f, 0.f};
     if (y == 0.f || z == 0.f) return r;   // no counted place, or none that the teacher weighs: nothing to learn
-    r.loss = x / y + (logf(z) - logf(y));
+    r.loss = x / y * 0.69314718055994531f + (logf(z) - logf(y));
     r.cs = g * a.inv_tau / z;
     r.ct = g * a.inv_tau / y;
     return r;
 }
 
 // One row per group of T threads (T = 32: NT / 32 rows per CTA; else T == NT), in registers.
-template <typename TT, int VEC, int T, int NV, int NT>
+template <typename TT, int VEC, bool EDGE, int T, int NV, int NT>
 __global__ void __launch_bounds__(NT) distill_kernel(const __grid_constant__ DistillArgs a)
 {
     __shared__ float4 red1[32], red2[32];
@@ -151,24 +166,23 @@ __global__ void __launch_bounds__(NT) distill_kernel(const __grid_constant__ Dis
     const float* sp = a.s + (int64_t)row * a.ld_s;
     const TT* tp = static_cast<const TT*>(a.t) + (int64_t)row * a.ld_t;
     const int32_t* lp = a.list ? a.list + (int64_t)row * a.ld_list : nullptr;
+    // columns are taken from the 4-place boundary at or before the row's start, so that rows of an odd
+    // stride still move 16 bytes at a time (single places cost twice the time)
+    const int c0 = EDGE ? -((a.off0 + row * a.off_step) & 3) : 0;
     float s[NV][VEC], f[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * T + t) * VEC;
-        if (c < a.k) {
-            distill_load<VEC>(sp + c, s[i]);
-            distill_load<VEC>(tp + c, f[i]);
-            if (lp) {
-                int32_t l[VEC];
-                distill_load<VEC>(lp + c, l);
+        const int c = c0 + (i * T + t) * VEC;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    if (l[e] < 0) s[i][e] = -CUDART_INF_F;
-            }
-        } else {
+        for (int e = 0; e < VEC; ++e) s[i][e] = -CUDART_INF_F;
+        if (c >= a.k) continue;
+        distill_load<VEC, EDGE>(sp, c, a.k, s[i]);
+        distill_load<VEC, EDGE>(tp, c, a.k, f[i]);
+        int32_t l[VEC];
+        if (lp) distill_load<VEC, EDGE>(lp, c, a.k, l);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) s[i][e] = -CUDART_INF_F;
-        }
+        for (int e = 0; e < VEC; ++e)
+            if ((EDGE && (c + e < 0 || c + e >= a.k)) || (lp && l[e] < 0)) s[i][e] = -CUDART_INF_F;
     }
     float ms = -CUDART_INF_F, mt = -CUDART_INF_F;
 #pragma unroll
@@ -186,8 +200,8 @@ __global__ void __launch_bounds__(NT) distill_kernel(const __grid_constant__ Dis
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             const bool in = s[i][e] != -CUDART_INF_F;
-            const float d = (s[i][e] - ms) * a.inv_tau;
-            s[i][e] = in ? expf(d) : 0.f;
+            const float d = (s[i][e] - ms) * a.scale;
+            s[i][e] = in ? distill_exp2(d) : 0.f;
             z += s[i][e];
             float c = 0.f, w = 0.f;
             if (in && mt != -CUDART_INF_F) w = distill_weight(f[i][e], mt, a, c);
@@ -202,20 +216,25 @@ __global__ void __launch_bounds__(NT) distill_kernel(const __grid_constant__ Dis
     float* dp = a.ds + (int64_t)row * a.ld_ds;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * T + t) * VEC;
+        const int c = c0 + (i * T + t) * VEC;
         if (c >= a.k) continue;
         float v[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e)   // 0 where neither has weight, whatever a NaN elsewhere made of the factors
             v[e] = s[i][e] == 0.f && f[i][e] == 0.f ? 0.f : s[i][e] * r.cs - f[i][e] * r.ct;
-        if constexpr (VEC == 4)
-            *reinterpret_cast<float4*>(dp + c) = make_float4(v[0], v[1], v[2], v[3]);
-        else
-            dp[c] = v[0];
+        if (VEC == 4 && (!EDGE || (c >= 0 && c + 3 < a.k))) {
+            *reinterpret_cast<float4*>(dp + c) = make_float4(v[0], v[VEC / 4], v[VEC / 2], v[VEC - 1]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (!EDGE || (c + e >= 0 && c + e < a.k)) dp[c + e] = v[e];
+        }
     }
 }
 
-// Rows of any length: one CTA per row, three sweeps (maxima, sums, gradient).
+// Rows of any length: one CTA per row, two sweeps.  In the first a thread keeps running maxima and
+// sums, rescaled when a batch of places raises a maximum; the CTA then brings its threads' sums to the
+// row's maxima and joins them; the second writes the gradient.
 template <typename TT, int NT>
 __global__ void __launch_bounds__(NT) distill_long_kernel(const __grid_constant__ DistillArgs a)
 {
@@ -224,47 +243,78 @@ __global__ void __launch_bounds__(NT) distill_long_kernel(const __grid_constant_
     const float* sp = a.s + (int64_t)row * a.ld_s;
     const TT* tp = static_cast<const TT*>(a.t) + (int64_t)row * a.ld_t;
     const int32_t* lp = a.list ? a.list + (int64_t)row * a.ld_list : nullptr;
-    auto score = [&](int c) { return lp && lp[c] < 0 ? -CUDART_INF_F : sp[c]; };
-    auto teacher = [&](int c) {
-        if constexpr (sizeof(TT) == 2) return __bfloat162float(tp[c]);
-        else return (float)tp[c];
+    constexpr int BATCH = 8;
+    float s[BATCH], v[BATCH];
+    auto read = [&](int64_t c0) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int64_t c = c0 + (int64_t)i * NT;
+            s[i] = c < a.k ? sp[c] : -CUDART_INF_F;
+            v[i] = c < a.k ? (float)tp[c] : 0.f;
+            if (lp && c < a.k && lp[c] < 0) s[i] = -CUDART_INF_F;
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+            if (s[i] == -CUDART_INF_F) v[i] = a.weights ? 0.f : -CUDART_INF_F;
     };
-    float ms = -CUDART_INF_F, mt = -CUDART_INF_F;
-#pragma unroll 4
-    for (int c = threadIdx.x; c < a.k; c += NT) {
-        const float s = score(c);
-        const float v = teacher(c);
-        ms = fmaxf(ms, s);
-        if (s != -CUDART_INF_F) mt = fmaxf(mt, v);
+    // to maxima m and n: exponents shift by (m - ms) and, for logits, (n - mt); with nothing summed yet the
+    // old maximum is -inf and the sums are zero whatever they are scaled by
+    float ms = -CUDART_INF_F, mt = -CUDART_INF_F, z = 0.f, y = 0.f, x = 0.f;
+    auto raise = [&](float m, float n) {
+        if (m > ms) {
+            const float up = ms == -CUDART_INF_F ? 0.f : (m - ms) * a.scale;
+            z *= distill_exp2(-up);
+            x = fmaf(y, up, x);
+            ms = m;
+        }
+        if (!a.weights && n > mt) {
+            const float up = mt == -CUDART_INF_F ? 0.f : (n - mt) * a.scale, f = distill_exp2(-up);
+            x = (x - y * up) * f;
+            y *= f;
+            mt = n;
+        }
+    };
+    for (int64_t c0 = threadIdx.x; c0 < a.k; c0 += (int64_t)BATCH * NT) {
+        read(c0);
+        float m = ms, n = mt;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            m = fmaxf(m, s[i]);
+            n = fmaxf(n, v[i]);
+        }
+        raise(m, n);
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            if (s[i] == -CUDART_INF_F) continue;
+            const float d = (s[i] - ms) * a.scale;
+            z += distill_exp2(d);
+            float lg, w = 0.f;
+            if (a.weights || mt != -CUDART_INF_F) w = distill_weight(v[i], mt, a, lg);
+            y += w;
+            if (w != 0.f) x = fmaf(w, lg - d, x);
+        }
     }
-    distill_max2<NT>(ms, mt, red1);
-    float z = 0.f, y = 0.f, x = 0.f;
-#pragma unroll 4
-    for (int c = threadIdx.x; c < a.k; c += NT) {
-        const float s = score(c);
-        const float v = teacher(c);
-        if (s == -CUDART_INF_F) continue;
-        const float d = (s - ms) * a.inv_tau;
-        z += expf(d);
-        if (mt == -CUDART_INF_F) continue;
-        float lg;
-        const float w = distill_weight(v, mt, a, lg);
-        y += w;
-        if (w != 0.f) x = fmaf(w, lg - d, x);
-    }
+    float m = ms, n = mt;
+    distill_max2<NT>(m, n, red1);
+    raise(m, n);
     distill_sum3<NT>(z, y, x, red2);
     const DistillRow r = distill_row(z, y, x, a.g ? a.g[row] : 1.f, a);
     if (threadIdx.x == 0 && a.loss) a.loss[row] = r.loss;
     if (!a.ds) return;
     float* dp = a.ds + (int64_t)row * a.ld_ds;
-#pragma unroll 4
-    for (int c = threadIdx.x; c < a.k; c += NT) {
-        const float s = score(c);
-        const float v = teacher(c);
-        float lg, out = 0.f;
-        if (s != -CUDART_INF_F && mt != -CUDART_INF_F)
-            out = expf((s - ms) * a.inv_tau) * r.cs - distill_weight(v, mt, a, lg) * r.ct;
-        dp[c] = out;
+    for (int64_t c0 = threadIdx.x; c0 < a.k; c0 += (int64_t)BATCH * NT) {
+        read(c0);
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int64_t c = c0 + (int64_t)i * NT;
+            if (c >= a.k) continue;
+            float lg, out = 0.f;
+            if (s[i] != -CUDART_INF_F) {
+                out = distill_exp2((s[i] - ms) * a.scale) * r.cs;
+                if (a.weights || mt != -CUDART_INF_F) out -= distill_weight(v[i], mt, a, lg) * r.ct;
+            }
+            dp[c] = out;
+        }
     }
 }
 

@@ -35,36 +35,50 @@ struct NormArgs {
     float eps;
 };
 
-__device__ __forceinline__ float norm_load(const float* p) { return *p; }
-__device__ __forceinline__ float norm_load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+// VEC consecutive elements as loaded (VEC 8: 16-byte aligned rows; VEC 1: any), and as fp32.
+template <typename TX, int VEC>
+struct NormRaw {
+    TX v;
+    __device__ __forceinline__ void load(const TX* p) { v = *p; }
+    __device__ __forceinline__ void get(float* f) const { f[0] = (float)v; }
+};
 
-// VEC consecutive elements as fp32 (VEC 8: 16-byte aligned rows; VEC 1: any).
-template <int VEC>
-__device__ __forceinline__ void norm_load_vec(const float* p, float* v)
-{
-    if constexpr (VEC == 8) {
-        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-        v[0] = *p;
+template <>
+struct NormRaw<float, 8> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p)
+    {
+        a = *reinterpret_cast<const float4*>(p);
+        b = *reinterpret_cast<const float4*>(p + 4);
     }
-}
+    __device__ __forceinline__ void get(float* f) const
+    {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+};
 
-template <int VEC>
-__device__ __forceinline__ void norm_load_vec(const __nv_bfloat16* p, float* v)
-{
-    if constexpr (VEC == 8) {
-        const uint4 a = *reinterpret_cast<const uint4*>(p);
+template <>
+struct NormRaw<__nv_bfloat16, 8> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void get(float* f) const
+    {
         const uint32_t u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(u[i] << 16);
-            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            f[2 * i] = __uint_as_float(u[i] << 16);
+            f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
         }
-    } else {
-        v[0] = __bfloat162float(*p);
     }
+};
+
+template <int VEC, typename TX>
+__device__ __forceinline__ void norm_load_vec(const TX* p, float* f)
+{
+    NormRaw<TX, VEC> r;
+    r.load(p);
+    r.get(f);
 }
 
 template <int VEC>
@@ -95,6 +109,8 @@ __device__ __forceinline__ void norm_store_vec(__nv_bfloat16* p, const float* v)
 }
 
 // Sum of (a, b) over the T threads of a row group: lanes of one warp, or the whole CTA (T == NT).
+// `red` (32 entries) must not be in use by a sum that some thread may still be reading: callers
+// alternate between two.
 template <int T>
 __device__ __forceinline__ void norm_group_sum(float& a, float& b, float2* red)
 {
@@ -104,50 +120,56 @@ __device__ __forceinline__ void norm_group_sum(float& a, float& b, float2* red)
         b += __shfl_xor_sync(0xffffffffu, b, o);
     }
     if constexpr (T > 32) {
-        constexpr int NW = T / 32;
-        __syncthreads();   // red is free
+        constexpr int NW = T / 32;   // a power of two: every warp adds the same tree, every lane ends with the sum
         if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
         __syncthreads();
-        a = 0.f;
-        b = 0.f;
+        const float2 v = red[threadIdx.x & (NW - 1)];
+        a = v.x;
+        b = v.y;
 #pragma unroll
-        for (int i = 0; i < NW; ++i) {
-            const float2 v = red[i];
-            a += v.x;
-            b += v.y;
+        for (int o = NW / 2; o > 0; o >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, o);
+            b += __shfl_xor_sync(0xffffffffu, b, o);
         }
     }
 }
 
 // NT threads per CTA in groups of T; element e of thread t of a group: column ((e / VEC) * T + t) * VEC + e % VEC.
-template <typename TX, typename TY, int VEC, int T, int NV, int NT>
+// A group takes R rows (NT / T apart), all asked for before the first is used.
+template <typename TX, typename TY, int VEC, int T, int NV, int NT, int R>
 __global__ void __launch_bounds__(NT) layer_norm_kernel(const __grid_constant__ NormArgs a)
 {
-    __shared__ float2 red[32];
+    __shared__ float2 red[2][32];
     constexpr int G = NT / T;   // rows of a CTA at once
     const int t = threadIdx.x % T, g = threadIdx.x / T;
     const float inv_d = 1.f / (float)a.d;
-    for (int64_t row0 = (int64_t)blockIdx.x * G; row0 < a.n; row0 += (int64_t)gridDim.x * G) {
-        const int64_t row = row0 + g;
-        const bool live = row < a.n;
-        const TX* x = static_cast<const TX*>(a.x) + row * a.ld_x;
-        float v[NV][VEC];
+    const int64_t row0 = (int64_t)blockIdx.x * (G * R) + g;
+    NormRaw<TX, VEC> raw[R][NV];
+#pragma unroll
+    for (int k = 0; k < R; ++k)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
+            const int64_t row = row0 + k * G;
             const int c = (i * T + t) * VEC;
-            if (live && c < a.d) {
-                norm_load_vec<VEC>(x + c, v[i]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
-            }
+            if (row < a.n && c < a.d) raw[k][i].load(static_cast<const TX*>(a.x) + row * a.ld_x + c);
         }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        const int64_t row = row0 + k * G;
+        const bool live = row < a.n;
+        float v[NV][VEC];
         float s = 0.f, unused = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i) {
+            const bool in = live && (i * T + t) * VEC < a.d;
+            raw[k][i].get(v[i]);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) s += v[i][e];
-        norm_group_sum<T>(s, unused, red);
+            for (int e = 0; e < VEC; ++e) {
+                v[i][e] = in ? v[i][e] : 0.f;
+                s += v[i][e];
+            }
+        }
+        norm_group_sum<T>(s, unused, red[0]);
         const float mu = s * inv_d;
         float q = 0.f;
 #pragma unroll
@@ -160,7 +182,7 @@ __global__ void __launch_bounds__(NT) layer_norm_kernel(const __grid_constant__ 
             }
         }
         unused = 0.f;
-        norm_group_sum<T>(q, unused, red);
+        norm_group_sum<T>(q, unused, red[1]);
         const float r = 1.f / sqrtf(fmaf(q, inv_d, a.eps));
         if (!live) continue;
         if (t == 0) {
@@ -184,57 +206,73 @@ __global__ void __launch_bounds__(NT) layer_norm_kernel(const __grid_constant__ 
     }
 }
 
-// TX: the type of x and dx, TY: of dy.  DX: dx is written, DW: the partial sums are.
+// TX: the type of x and dx, TY: of dy.  A group walks its rows with the next one's loads in flight
+// behind the current one's sums: without that, a group waits out the memory's latency once a row.
 template <typename TX, typename TY, int VEC, int T, int NV, int NT>
 __global__ void __launch_bounds__(NT) layer_norm_bwd_kernel(const __grid_constant__ NormArgs a)
 {
-    __shared__ float2 red[32];
+    __shared__ float2 red[2][32];
     constexpr int G = NT / T;
     const int t = threadIdx.x % T, g = threadIdx.x / T;
     const float inv_d = 1.f / (float)a.d;
-    float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
+    float dw[NV][VEC], db[NV][VEC];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * T + t) * VEC;
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            w[i][e] = 1.f;
-            dw[i][e] = db[i][e] = 0.f;
-        }
-        if (a.w && c < a.d) norm_load_vec<VEC>(a.w + c, w[i]);
-    }
-    for (int64_t row0 = (int64_t)blockIdx.x * G; row0 < a.n; row0 += (int64_t)gridDim.x * G) {
-        const int64_t row = row0 + g;
-        const bool live = row < a.n;
+        for (int e = 0; e < VEC; ++e) dw[i][e] = db[i][e] = 0.f;
+    NormRaw<TX, VEC> rx[NV];
+    NormRaw<TY, VEC> ry[NV];
+    float mu_next = 0.f, r_next = 0.f;
+    auto read = [&](int64_t row) {
+        if (row >= a.n) return;
         const TX* x = static_cast<const TX*>(a.x) + row * a.ld_x;
         const TY* dy = static_cast<const TY*>(a.dy) + row * a.ld_dy;
-        float xh[NV][VEC], gy[NV][VEC];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * T + t) * VEC;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) xh[i][e] = gy[i][e] = 0.f;
-            if (live && c < a.d) {
-                norm_load_vec<VEC>(x + c, xh[i]);
-                norm_load_vec<VEC>(dy + c, gy[i]);
+            if (c < a.d) {
+                rx[i].load(x + c);
+                ry[i].load(dy + c);
             }
         }
-        const float mu = live ? a.mean_in[row] : 0.f, r = live ? a.rstd_in[row] : 0.f;
+        mu_next = a.mean_in[row];
+        r_next = a.rstd_in[row];
+    };
+    const int64_t step = (int64_t)gridDim.x * G;
+    read((int64_t)blockIdx.x * G + g);
+    int odd = 0;
+    for (int64_t row0 = (int64_t)blockIdx.x * G; row0 < a.n; row0 += step, odd ^= 1) {
+        const int64_t row = row0 + g;
+        const bool live = row < a.n;
+        float xh[NV][VEC], gy[NV][VEC];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            rx[i].get(xh[i]);
+            ry[i].get(gy[i]);
+        }
+        const float mu = mu_next, r = r_next;
+        read(row + step);
         float s1 = 0.f, s2 = 0.f;   // sums of g and of g xh
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const bool in = live && (i * T + t) * VEC < a.d;
+            const int c = (i * T + t) * VEC;
+            const bool in = live && c < a.d;
+            float w[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) w[e] = 1.f;
+            if (a.w && c < a.d) norm_load_vec<VEC>(a.w + c, w);   // from L1 after the first row
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 xh[i][e] = in ? (xh[i][e] - mu) * r : 0.f;
+                gy[i][e] = in ? gy[i][e] : 0.f;
                 dw[i][e] = fmaf(gy[i][e], xh[i][e], dw[i][e]);
                 db[i][e] += gy[i][e];
-                gy[i][e] *= w[i][e];
+                gy[i][e] *= w[e];
                 s1 += gy[i][e];
                 s2 = fmaf(gy[i][e], xh[i][e], s2);
             }
         }
-        norm_group_sum<T>(s1, s2, red);
+        norm_group_sum<T>(s1, s2, red[odd]);
         const float m1 = s1 * inv_d, m2 = s2 * inv_d;
         if (!live || !a.out) continue;
         TX* dx = static_cast<TX*>(a.out) + row * a.ld_out;
@@ -247,6 +285,7 @@ __global__ void __launch_bounds__(NT) layer_norm_bwd_kernel(const __grid_constan
             norm_store_vec<VEC>(dx + c, gy[i]);
         }
     }
+    grid_dep_launch();   // the summing kernel may start its prologue
     if (!a.part) return;
     // join the CTA's row groups in order of their number, then one partial row per CTA
     float* out = a.part + (int64_t)blockIdx.x * 2 * a.d;
@@ -301,6 +340,7 @@ __global__ void __launch_bounds__(1024) layer_norm_dw_kernel(const float* part, 
     grid_dep_wait();
     float s = 0.f;
     if (c < 2 * d)
+#pragma unroll 8
         for (int i = ty; i < n_part; i += 32) s += part[(int64_t)i * 2 * d + c];
     sh[ty][tx] = s;
     __syncthreads();

@@ -39,28 +39,41 @@ bool rows_aligned(const void* p, int32_t type, int64_t ld, int64_t n)
 
 // ------------------------------------------------------------- layer norm
 
-// CTAs of the backward pass: as many row groups as fill the GPU (2 CTAs an SM: their partial sums
-// are written and read once more, so more CTAs cost more), fewer for short matrices.
-int32_t norm_bwd_ctas(int64_t n, int32_t groups)
+// CTAs of the backward pass with `threads` threads that take `groups` rows at once: as many as are
+// resident (1024 threads an SM: the rows held and read ahead take some 64 registers), fewer where
+// that leaves a CTA under 8 rows a group, since each CTA's partial sums (8 bytes a column) are
+// written and read once more.
+int32_t norm_bwd_ctas(int64_t n, int32_t groups, int32_t threads)
 {
-    return (int32_t)std::max<int64_t>(1, std::min<int64_t>((n + groups - 1) / groups, 2 * 148));
+    const int64_t resident = int64_t(148) * (1024 / threads);
+    return (int32_t)std::max<int64_t>(1, std::min((n + 8 * groups - 1) / (8 * groups), resident));
 }
+
+// The most CTAs any row group takes (narrow rows in groups of one warp or less: 256 threads).
+constexpr int64_t kNormMaxCtas = 148 * 8;
 
 template <typename TX, typename TY, int VEC, int T, int NV, int NT>
 dsa_status norm_launch(const NormArgs& a, bool backward, int32_t* n_part, cudaStream_t st)
 {
     constexpr int G = NT / T;
     if (backward) {
-        *n_part = norm_bwd_ctas(a.n, G);
+        *n_part = norm_bwd_ctas(a.n, G, NT);
         DSA_LAUNCH(kProfNorm, st, layer_norm_bwd_kernel<TX, TY, VEC, T, NV, NT><<<*n_part, NT, 0, st>>>(a));
+        return launched();
+    }
+    // narrow rows: four a group in flight once that still fills the GPU (32768 x 128: 9.0 us with one)
+    constexpr int R = NV * VEC <= 8 && T <= 32 ? 4 : 1;
+    if (R == 1 || a.n < int64_t(148) * G * R) {
+        DSA_LAUNCH(kProfNorm, st,
+                   layer_norm_kernel<TX, TY, VEC, T, NV, NT, 1><<<(unsigned)((a.n + G - 1) / G), NT, 0, st>>>(a));
     } else {
-        const int64_t ctas = std::min<int64_t>((a.n + G - 1) / G, int64_t(148) * (2048 / NT));
-        DSA_LAUNCH(kProfNorm, st, layer_norm_kernel<TX, TY, VEC, T, NV, NT><<<(unsigned)ctas, NT, 0, st>>>(a));
+        DSA_LAUNCH(kProfNorm, st, layer_norm_kernel<TX, TY, VEC, T, NV, NT, R>
+                   <<<(unsigned)((a.n + G * R - 1) / (G * R)), NT, 0, st>>>(a));
     }
     return launched();
 }
 
-// The row group of a width: as few threads as hold the row in at most 16 registers a thread, so a
+// The row group of a width: as few threads as hold the row in 8 registers a thread or so, so a
 // narrow row costs no cross-warp step (128 values of a key: 16 lanes with one 16-byte load each).
 template <typename TX, typename TY>
 dsa_status norm_pick(const NormArgs& a, bool vec, bool bwd, int32_t* np, cudaStream_t st)
@@ -70,18 +83,19 @@ dsa_status norm_pick(const NormArgs& a, bool vec, bool bwd, int32_t* np, cudaStr
         if (a.d <= 64) return norm_launch<TX, TY, 8, 8, 1, 256>(a, bwd, np, st);
         if (a.d <= 128) return norm_launch<TX, TY, 8, 16, 1, 256>(a, bwd, np, st);
         if (a.d <= 256) return norm_launch<TX, TY, 8, 32, 1, 256>(a, bwd, np, st);
-        if (a.d <= 512) return norm_launch<TX, TY, 8, 32, 2, 256>(a, bwd, np, st);
         if (a.d <= 1024) return norm_launch<TX, TY, 8, 128, 1, 128>(a, bwd, np, st);
         if (a.d <= 2048) return norm_launch<TX, TY, 8, 256, 1, 256>(a, bwd, np, st);
-        if (a.d <= 4096) return norm_launch<TX, TY, 8, 256, 2, 256>(a, bwd, np, st);
-        if (a.d <= 8192) return norm_launch<TX, TY, 8, 512, 2, 512>(a, bwd, np, st);
+        if (a.d <= 4096) return norm_launch<TX, TY, 8, 512, 1, 512>(a, bwd, np, st);
+        if (a.d <= 8192) return norm_launch<TX, TY, 8, 1024, 1, 1024>(a, bwd, np, st);
         return norm_launch<TX, TY, 8, 1024, 2, 1024>(a, bwd, np, st);
     }
     if (a.d <= 32) return norm_launch<TX, TY, 1, 32, 1, 256>(a, bwd, np, st);
     if (a.d <= 128) return norm_launch<TX, TY, 1, 32, 4, 256>(a, bwd, np, st);
-    if (a.d <= 512) return norm_launch<TX, TY, 1, 32, 16, 256>(a, bwd, np, st);
-    if (a.d <= 2048) return norm_launch<TX, TY, 1, 256, 8, 256>(a, bwd, np, st);
-    if (a.d <= 8192) return norm_launch<TX, TY, 1, 512, 16, 512>(a, bwd, np, st);
+    if (a.d <= 256) return norm_launch<TX, TY, 1, 32, 8, 256>(a, bwd, np, st);
+    if (a.d <= 1024) return norm_launch<TX, TY, 1, 256, 4, 256>(a, bwd, np, st);
+    if (a.d <= 2048) return norm_launch<TX, TY, 1, 512, 4, 512>(a, bwd, np, st);
+    if (a.d <= 5120) return norm_launch<TX, TY, 1, 1024, 5, 1024>(a, bwd, np, st);
+    if (a.d <= 8192) return norm_launch<TX, TY, 1, 1024, 8, 1024>(a, bwd, np, st);
     return norm_launch<TX, TY, 1, 1024, 16, 1024>(a, bwd, np, st);
 }
 
@@ -94,36 +108,45 @@ dsa_status norm_dispatch(const NormArgs& a, int32_t tx, int32_t ty, bool vec, bo
                           : norm_pick<__nv_bfloat16, __nv_bfloat16>(a, vec, bwd, np, st);
 }
 
-// Partial sums of the weight's and bias's gradients: the most CTAs any row group of the width takes.
+// Partial sums of the weight's and bias's gradients, for the most CTAs the row count and width take:
+// 256 threads (128 to 1024 columns: 128 threads) and one row a CTA are the least.
+size_t norm_part_floats(int64_t n, int32_t d)
+{
+    return size_t(std::min<int64_t>(std::max<int64_t>(1, (n + 7) / 8), kNormMaxCtas)) * 2 * d;
+}
+
 size_t norm_ws_bytes(int64_t n, int32_t d)
 {
     Carver c{nullptr};
-    c.take<float>(size_t(norm_bwd_ctas(n, 1)) * 2 * d);
+    c.take<float>(norm_part_floats(n, d));
     return c.off;
 }
 
 // ------------------------------------------------------------ distillation
 
-template <typename TT, int VEC, int T, int NV, int NT>
+template <typename TT, int VEC, bool EDGE, int T, int NV, int NT>
 dsa_status distill_launch(const DistillArgs& a, cudaStream_t st)
 {
     constexpr int R = NT / T;
-    DSA_LAUNCH(kProfDistill, st, distill_kernel<TT, VEC, T, NV, NT><<<(a.n + R - 1) / R, NT, 0, st>>>(a));
+    DSA_LAUNCH(kProfDistill, st, distill_kernel<TT, VEC, EDGE, T, NV, NT><<<(a.n + R - 1) / R, NT, 0, st>>>(a));
     return launched();
 }
 
-template <typename TT, int VEC>
+template <typename TT, int VEC, bool EDGE>
 dsa_status distill_pick(const DistillArgs& a, cudaStream_t st)
 {
+    // 16 places a thread or so: with 8 the two joint reductions were a third of the instructions
     constexpr int U = 4 / VEC;   // registers' worth of a 4-wide load
-    if (a.k <= 128) return distill_launch<TT, VEC, 32, 1 * U, 256>(a, st);
-    if (a.k <= 512) return distill_launch<TT, VEC, 32, 4 * U, 256>(a, st);
-    if (a.k <= 1024) return distill_launch<TT, VEC, 128, 2 * U, 128>(a, st);
-    if (a.k <= 2048) return distill_launch<TT, VEC, 256, 2 * U, 256>(a, st);
-    if (a.k <= 4096) return distill_launch<TT, VEC, 256, 4 * U, 256>(a, st);
-    if (a.k <= 8192) return distill_launch<TT, VEC, 512, 4 * U, 512>(a, st);
-    if (a.k <= kDistillRegCols) return distill_launch<TT, VEC, 1024, 4 * U, 1024>(a, st);
-    DSA_LAUNCH(kProfDistill, st, distill_long_kernel<TT, 1024><<<a.n, 1024, 0, st>>>(a));
+    const int32_t k = EDGE ? a.k + 3 : a.k;   // columns from the boundary before the row
+    if (k <= 128) return distill_launch<TT, VEC, EDGE, 32, 1 * U, 256>(a, st);
+    if (k <= 512) return distill_launch<TT, VEC, EDGE, 32, 4 * U, 256>(a, st);
+    if (k <= 1024) return distill_launch<TT, VEC, EDGE, 64, 4 * U, 64>(a, st);
+    if (k <= 2048) return distill_launch<TT, VEC, EDGE, 128, 4 * U, 128>(a, st);
+    if (k <= 4096) return distill_launch<TT, VEC, EDGE, 256, 4 * U, 256>(a, st);
+    if (k <= 8192) return distill_launch<TT, VEC, EDGE, 512, 4 * U, 512>(a, st);
+    if (k <= 16384) return distill_launch<TT, VEC, EDGE, 1024, 4 * U, 1024>(a, st);
+    if (k <= kDistillRegCols) return distill_launch<TT, VEC, EDGE, 1024, 5 * U, 1024>(a, st);
+    DSA_LAUNCH(kProfDistill, st, distill_long_kernel<TT, 512><<<a.n, 512, 0, st>>>(a));
     return launched();
 }
 
@@ -337,7 +360,7 @@ dsa_status dsa_layer_norm_backward(int64_t n, int32_t d, const void* dy, int32_t
     NormArgs a{};
     a.x = x; a.ld_x = ld_x; a.dy = dy; a.ld_dy = ld_dy; a.out = dx; a.ld_out = ld_dx; a.w = weight;
     a.mean_in = mean; a.rstd_in = rstd; a.n = n; a.d = d;
-    a.part = dweight || dbias ? c.take<float>(size_t(norm_bwd_ctas(n, 1)) * 2 * d) : nullptr;
+    a.part = dweight || dbias ? c.take<float>(norm_part_floats(n, d)) : nullptr;
     const bool vec = d % 8 == 0 && rows_aligned(x, x_type, ld_x, n) && rows_aligned(dy, dy_type, ld_dy, n) &&
                      (!dx || rows_aligned(dx, x_type, ld_dx, n)) && (reinterpret_cast<uintptr_t>(weight) & 15) == 0;
     int32_t n_part = 0;
@@ -369,14 +392,23 @@ dsa_status dsa_distill_topk(int32_t n, int32_t k, const float* scores, int64_t l
     a.g = grad_loss; a.loss = loss; a.ds = dscores; a.ld_ds = ld_dscores; a.n = n; a.k = k;
     a.weights = teacher_kind == DSA_TEACHER_WEIGHTS ? 1 : 0;
     a.inv_tau = 1.f / temperature;
-    // four places a load where every row starts on a 16-byte boundary (the teacher's 16-bit rows: 8 bytes)
-    const bool vec = k % 4 == 0 && rows_aligned(scores, DSA_FP32, ld_scores, n) &&
-                     rows_aligned(teacher, teacher_type, teacher_type == DSA_BF16 ? ld_teacher * 2 : ld_teacher, n) &&
-                     (!lists || rows_aligned(lists, DSA_FP32, ld_lists, n)) &&
-                     (!dscores || rows_aligned(dscores, DSA_FP32, ld_dscores, n));
+    a.scale = (float)(1.4426950408889634 / (double)temperature);
+    // four places a load where the arrays' rows lie alike against 4-place boundaries
+    const auto place = [](const void* p, int64_t size) { return int32_t(reinterpret_cast<uintptr_t>(p) / size % 4); };
+    a.off0 = place(scores, 4);
+    a.off_step = int32_t(ld_scores % 4);
+    const auto alike = [&](const void* p, int64_t size, int64_t ld) {
+        return !p || (place(p, size) == a.off0 && (n == 1 || int32_t(ld % 4) == a.off_step));
+    };
+    const bool vec = alike(teacher, type_size(teacher_type), ld_teacher) && alike(lists, 4, ld_lists) &&
+                     alike(dscores, 4, ld_dscores);
+    const bool edge = k % 4 != 0 || a.off0 != 0 || (n > 1 && a.off_step != 0);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (teacher_type == DSA_FP32) return vec ? distill_pick<float, 4>(a, st) : distill_pick<float, 1>(a, st);
-    return vec ? distill_pick<__nv_bfloat16, 4>(a, st) : distill_pick<__nv_bfloat16, 1>(a, st);
+    if (teacher_type == DSA_FP32)
+        return !vec ? distill_pick<float, 1, false>(a, st) : edge ? distill_pick<float, 4, true>(a, st)
+                                                                  : distill_pick<float, 4, false>(a, st);
+    return !vec ? distill_pick<__nv_bfloat16, 1, false>(a, st) : edge ? distill_pick<__nv_bfloat16, 4, true>(a, st)
+                                                                      : distill_pick<__nv_bfloat16, 4, false>(a, st);
 }
 
 // ----------------------------------------------------- scores at listed keys
