@@ -58,10 +58,10 @@ __device__ __forceinline__ void distill_load(const X* p, int c, int k, V* v)
             const float4 a = __ldcs(reinterpret_cast<const float4*>(p + c));
             v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
         }
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = !EDGE || (c + e >= 0 && c + e < k) ? (V)p[c + e] : V(0);
+        for (int e = 0; e < VEC; ++e) v[e] = !EDGE || (c + e >= 0 && c + e < k) ? (V)p[c + e] : V(0);
+    }
 }
 
 // Joint reductions over the T threads of a row: a warp's lanes (T = 32) or the whole CTA.

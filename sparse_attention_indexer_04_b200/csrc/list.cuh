@@ -26,11 +26,33 @@ struct ListArgs {
     int32_t n_seqs, n_q, n_k, H, k;
 };
 
-// Usable list places of every query (one warp each): strictly ascending keys of the sequence up to
-// the first -1, of which those within the query's prefix count.  A key outside the sequence, not
-// above its predecessor or behind the padding ends the list and records kErrBadRow (detail t).
-__global__ void list_rows_kernel(const int32_t* lists, int32_t k, const int32_t* q_off, const int32_t* k_off,
-                                 const int32_t* q_pos, int32_t n_seqs, int32_t n_q, RowDesc* rows, uint32_t* status)
+constexpr int kPosBlock = 256;  // keys that share a base of row positions
+constexpr int kDkKeys = 256;   // keys of a block of the dense dK pass
+
+// Key blocks over all sequences: sequence b's first is unit_base(b), which leaves it at least as many
+// as it has, without a table.  find_unit: the sequence of a block.
+__device__ __forceinline__ int unit_base(const int32_t* k_off, int b) { return k_off[b] / kDkKeys + b; }
+
+__device__ __forceinline__ int find_unit(const int32_t* k_off, int n_seqs, int unit)
+{
+    int lo = 0, hi = n_seqs - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (unit_base(k_off, mid) <= unit) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// One warp per query.  rows[t]: the usable list places, which are strictly ascending keys of the
+// sequence up to the first -1, of which those within the query's prefix count; a key outside the
+// sequence, not above its predecessor or behind the padding ends the list and records kErrBadRow
+// (detail t).  edge (may be NULL): per block of kDkKeys keys the first usable place at or behind the
+// block's start, edge[b][n_q] for blocks 0 .. n_blocks.  `quads`: rows are read four places at a time.
+__global__ void __launch_bounds__(256) list_rows_kernel(const int32_t* lists, int32_t k, int32_t quads,
+                                                        const int32_t* q_off, const int32_t* k_off,
+                                                        const int32_t* q_pos, int32_t n_seqs, int32_t n_q,
+                                                        RowDesc* rows, uint16_t* edge, int32_t n_blocks,
+                                                        uint32_t* status)
 {
     const int t = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (t >= n_q) return;
@@ -38,21 +60,58 @@ __global__ void list_rows_kernel(const int32_t* lists, int32_t k, const int32_t*
     const int L = k_off[seq + 1] - k_off[seq];
     const int lim = eligible_count(q_pos[t], L);
     const int32_t* l = lists + (int64_t)t * k;
-    int first_end = k, first_bad = k, first_far = k;
-    for (int i = lane; i < k; i += 32) {
-        const int32_t v = l[i];
-        const int32_t prev = i > 0 ? l[i - 1] : -1;
-        if (v < 0) { first_end = min(first_end, i); continue; }
+    int first_end = k, first_bad = k, first_far = k, carry = -1;
+    // place i holds v behind prev (the sequence's start: -1 < 0 passes for place 0)
+    auto look = [&](int i, int v, int prev) {
+        if (v < 0) { first_end = min(first_end, i); return; }
         if (v >= L || (i > 0 && (prev < 0 || prev >= v))) first_bad = min(first_bad, i);
         if (v >= lim) first_far = min(first_far, i);
-    }
+    };
+    // the block borders between place i - 1 and place i
+    auto borders = [&](int i, int v, int prev) {
+        const int lo = i > 0 ? prev / kDkKeys + 1 : 0, hi = v / kDkKeys;
+        for (int b = lo; b <= hi; ++b) edge[(int64_t)b * n_q + t] = (uint16_t)i;
+    };
+    auto sweep = [&](auto&& f, int n) {
+        carry = -1;
+        if (quads) {
+#pragma unroll 4
+            for (int i0 = 0; i0 < n; i0 += 128) {
+                const int i = i0 + 4 * lane;
+                const int4 v = i < k ? __ldg(reinterpret_cast<const int4*>(l + i)) : make_int4(-1, -1, -1, -1);
+                const int up = __shfl_up_sync(0xffffffffu, v.w, 1);
+                const int prev = lane == 0 ? carry : up;
+                carry = __shfl_sync(0xffffffffu, v.w, 31);
+                if (i < n) f(i, v.x, prev);
+                if (i + 1 < n) f(i + 1, v.y, v.x);
+                if (i + 2 < n) f(i + 2, v.z, v.y);
+                if (i + 3 < n) f(i + 3, v.w, v.z);
+            }
+        } else {
+#pragma unroll 4
+            for (int i0 = 0; i0 < n; i0 += 32) {
+                const int i = i0 + lane;
+                const int v = i < k ? __ldg(l + i) : -1;
+                const int up = __shfl_up_sync(0xffffffffu, v, 1);
+                const int prev = lane == 0 ? carry : up;
+                carry = __shfl_sync(0xffffffffu, v, 31);
+                if (i < n) f(i, v, prev);
+            }
+        }
+    };
+    sweep(look, k);
     first_end = __reduce_min_sync(0xffffffffu, first_end);
     first_bad = __reduce_min_sync(0xffffffffu, first_bad);
     first_far = __reduce_min_sync(0xffffffffu, first_far);
+    const int n = min(min(first_end, first_bad), first_far);
     if (lane == 0) {
         if (first_bad < k) record_error(status, kErrBadRow, (uint32_t)t);
-        rows[t] = RowDesc{t, seq, min(min(first_end, first_bad), first_far), t};
+        rows[t] = RowDesc{t, seq, n, t};
     }
+    if (!edge) return;
+    sweep(borders, n);   // from L1 or L2
+    const int last = n > 0 ? l[n - 1] / kDkKeys + 1 : 0;
+    for (int b = last + lane; b <= n_blocks; b += 32) edge[(int64_t)b * n_q + t] = (uint16_t)n;
 }
 
 }  // namespace dsa

@@ -24,24 +24,7 @@
 namespace dsa {
 
 constexpr int kDkThreads = 672;
-constexpr int kDkKeys = 256;
 constexpr int kDkMaxList = 8192;   // queries of one CTA at most
-
-// Per query and block of kDkKeys keys, the first list place at or behind the block's start:
-// edge[block][n_q], for blocks 0 .. max_blocks (the last row: the usable length).  One warp per query.
-__global__ void list_edges_kernel(const int32_t* lists, int32_t k, const RowDesc* rows, int32_t n_q, int32_t n_blocks,
-                                  uint16_t* edge)
-{
-    const int t = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (t >= n_q) return;
-    const int n = rows[t].ncols;
-    const int32_t* l = lists + (int64_t)t * k;
-    for (int i = lane; i <= n; i += 32) {
-        const int lo = i > 0 ? l[i - 1] / kDkKeys + 1 : 0;       // blocks that start behind place i - 1
-        const int hi = i < n ? l[i] / kDkKeys : n_blocks;        // and at or before place i
-        for (int b = lo; b <= hi; ++b) edge[(int64_t)b * n_q + t] = (uint16_t)i;
-    }
-}
 
 template <int D, int H>
 struct DkShape {
@@ -78,9 +61,6 @@ struct DkArgs {
     int32_t parts;
 };
 
-// First unit of sequence b: at least as many units as key blocks, without a table.
-__device__ __forceinline__ int dk_unit_base(const int32_t* k_off, int b) { return k_off[b] / kDkKeys + b; }
-
 template <int D, int H>
 __global__ void __launch_bounds__(kDkThreads, 1)
     list_dk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ DkArgs a)
@@ -94,16 +74,8 @@ __global__ void __launch_bounds__(kDkThreads, 1)
         return;
     }
     const int unit = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
-    // the unit's sequence and key block
-    int seq = 0;
-    {
-        int hi = a.l.n_seqs - 1;
-        while (seq < hi) {
-            const int mid = (seq + hi + 1) >> 1;
-            if (dk_unit_base(a.l.k_off, mid) <= unit) seq = mid; else hi = mid - 1;
-        }
-    }
-    const int blk = unit - dk_unit_base(a.l.k_off, seq);
+    const int seq = find_unit(a.l.k_off, a.l.n_seqs, unit);
+    const int blk = unit - unit_base(a.l.k_off, seq);
     const int kb = a.l.k_off[seq], L = a.l.k_off[seq + 1] - kb;
     const int s0 = blk * kDkKeys;
     if (s0 >= L) return;   // a unit without keys

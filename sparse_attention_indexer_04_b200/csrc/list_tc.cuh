@@ -26,8 +26,11 @@ namespace dsa {
 // half of the heads each).  Measured backward, 4096 queries x 2048 keys, H = 64: 64 heads a thread in two
 // groups 556 us, 16 heads a thread in one group 322 us (both with one issuer's other steps alike).
 constexpr int kListTcProducers = 4;
-constexpr int list_sets(bool bwd) { return bwd ? 4 : 2; }
-constexpr int list_threads(bool bwd) { return 32 * (1 + kListTcProducers + (bwd ? 1 : 0)) + 128 * list_sets(bwd); }
+constexpr int list_sets(int mode) { return mode ? 4 : 2; }
+constexpr int list_threads(int mode)
+{
+    return 32 * (1 + kListTcProducers + (mode ? 1 : 0) + (mode == 2 ? 4 : 0)) + 128 * list_sets(mode);
+}
 constexpr uint32_t kErrListAlign = 3;
 
 // Shared-memory matrix descriptor of an MN-major operand: rows of the K dimension are row_bytes
@@ -102,6 +105,14 @@ __device__ __forceinline__ bool tc_wait_warp(uint64_t* bar, uint32_t parity, uin
                                              volatile int32_t* abort_flag, bool alive)
 {
     return __all_sync(0xffffffffu, alive && tc_wait(bar, parity, status, where, abort_flag));
+}
+
+// 32 bytes in one store (p 32-byte aligned): whole memory sectors, although a warp's lanes write far apart.
+__device__ __forceinline__ void store_f32x8(float* p, const float* v)
+{
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
 }
 
 // Stores N (4, 8 or 16) consecutive 32-bit columns of this thread's TMEM lane and waits for them.
@@ -199,6 +210,14 @@ struct ListShape {
 struct ListTcArgs {
     ListArgs l;
     int32_t n_stages;
+    int32_t t0, t1;        // queries of the launch
+    // kListGradRows: the rows sum_h G[t,j,h] q[t,h], stored by key.  Key row s lists its rows from
+    // base[s / keys of a block] + off[s] on; before query t's come pre + the bits below t's.
+    float* part;
+    const uint32_t* bits;  // [words][n_k]
+    const uint16_t* pre;   // [words][n_k]
+    const uint32_t* off;   // [n_k]
+    const uint32_t* base;
 };
 
 __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b)
@@ -239,10 +258,14 @@ __device__ __forceinline__ void warp_transpose_sum(float* v, int lane)
     for (int o = N; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
 }
 
-template <int D, int HP, bool BWD>
-__global__ void __launch_bounds__(list_threads(BWD), 1)
+// What a launch makes: scores; dQ and dW; those and the rows G . Q that dK is summed from.
+enum : int { kListScores = 0, kListGrad = 1, kListGradRows = 2 };
+
+template <int D, int HP, int MODE>
+__global__ void __launch_bounds__(list_threads(MODE), 1)
     list_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ ListTcArgs a)
 {
+    constexpr bool BWD = MODE != kListScores, ROWS = MODE == kListGradRows;
     using SH = ListShape<D, HP>;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint32_t* status = a.l.status;
@@ -266,11 +289,13 @@ __global__ void __launch_bounds__(list_threads(BWD), 1)
     uint64_t* gfree = gfull + 2;               // [2] G has been read
     uint64_t* dqfull = gfree + 2;              // [2] dQ of a query is complete
     uint64_t* dqfree = dqfull + 2;             // [2] dQ has been read
-    uint64_t* drain = dqfree + 2;              // [2] one per issuing warp
+    uint64_t* dkfull = dqfree + 2;             // [2] a tile's rows of dK are complete
+    uint64_t* dkfree = dkfull + 2;             // [2] and read
+    uint64_t* drain = dkfree + 2;              // [2] one per issuing warp
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
     volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
 
-    constexpr int kEpi = 4 * list_sets(BWD);   // epilogue warps 2 .. kEpi + 1
+    constexpr int kEpi = 4 * list_sets(MODE);   // epilogue warps 2 .. kEpi + 1
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < n_stages; ++i) mbar_init(&full[i], kListTcProducers * 32);
@@ -284,6 +309,8 @@ __global__ void __launch_bounds__(list_threads(BWD), 1)
             mbar_init(&gfree[i], 1);
             mbar_init(&dqfull[i], 1);
             mbar_init(&dqfree[i], 512);
+            mbar_init(&dkfull[i], 1);
+            mbar_init(&dkfree[i], 128);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);
         *abort_flag = 0;
@@ -291,17 +318,18 @@ __global__ void __launch_bounds__(list_threads(BWD), 1)
         prefetch_tensormap(&tmQ);
     }
     // heads above H: zero rows that no load overwrites
-    for (uint32_t i = threadIdx.x; i < SH::align1k(2 * SH::QTILE) / 4; i += list_threads(BWD))
+    for (uint32_t i = threadIdx.x; i < SH::align1k(2 * SH::QTILE) / 4; i += list_threads(MODE))
         reinterpret_cast<uint32_t*>(sQ)[i] = 0u;
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    if (warp == 1) tmem_alloc(tmem_slot, 256);
+    constexpr uint32_t kCols = ROWS ? 512 : 256;   // S 2 x 64, dQ 2 x 64, rows of dK 2 x 128
+    if (warp == 1) tmem_alloc(tmem_slot, kCols);
     grid_dep_wait();   // the rows come from the set-up kernel
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t tS = tmem, tDQ = tmem + 128;
-    const int n_q = a.l.n_q, H = a.l.H, k = a.l.k, step = gridDim.x;
+    const int t0 = a.t0 + blockIdx.x, n_q = a.t1, H = a.l.H, k = a.l.k, step = gridDim.x;
     const RowDesc none{0, 0, 0, 0};
 
     if (warp == 0 || (warp >= 2 + kEpi && warp < 5 + kEpi)) {
@@ -320,8 +348,8 @@ __global__ void __launch_bounds__(list_threads(BWD), 1)
         uint32_t phase = 0;
         int q_issued = 0;
         bool alive = true;
-        RowDesc nx = (int)blockIdx.x < n_q ? a.l.rows[blockIdx.x] : none;
-        for (int t = blockIdx.x; t < n_q && alive; t += step) {
+        RowDesc nx = t0 < n_q ? a.l.rows[t0] : none;
+        for (int t = t0; t < n_q && alive; t += step) {
             const RowDesc r = nx;
             if (t + step < n_q) nx = a.l.rows[t + step];
             const int nt = (r.ncols + 127) >> 7;
@@ -381,8 +409,8 @@ __global__ void __launch_bounds__(list_threads(BWD), 1)
         uint32_t phase = 0;
         int n = 0, it = 0;     // tiles and non-empty queries so far
         bool alive = true;
-        int nx = (int)blockIdx.x < n_q ? a.l.rows[blockIdx.x].ncols : 0;
-        for (int t = blockIdx.x; t < n_q && alive; t += step) {
+        int nx = t0 < n_q ? a.l.rows[t0].ncols : 0;
+        for (int t = t0; t < n_q && alive; t += step) {
             const int nt = __shfl_sync(0xffffffffu, (nx + 127) >> 7, 0);
             if (t + step < n_q) nx = a.l.rows[t + step].ncols;
             if (nt == 0) continue;
@@ -405,7 +433,7 @@ __global__ void __launch_bounds__(list_threads(BWD), 1)
                                kk > 0 ? 1u : 0u);
                     }
                     tc_commit(&sfull[b]);
-                    if (i == nt - 1) tc_commit(&qempty[qb]);
+                    if (!ROWS && i == nt - 1) tc_commit(&qempty[qb]);
                     if (!BWD) tc_commit(&kempty[stage]);
                 }
                 __syncwarp();
@@ -424,11 +452,14 @@ __global__ void __launch_bounds__(list_threads(BWD), 1)
         const uint32_t idQ = idesc_bf16_f32(128, HP) | kIdescAMn | kIdescBMn;
         const uint64_t dKt = smem_desc_mnmajor(smem_u32(sK), SH::ROWB, SH::KBOX);
         const uint64_t dGt = smem_desc_mnmajor(smem_u32(sG), 128, 0);
+        [[maybe_unused]] const uint32_t idK = idesc_bf16_f32(128, D) | kIdescBMn;
+        [[maybe_unused]] const uint64_t dGk = smem_desc_kmajor(smem_u32(sG), 128);
+        [[maybe_unused]] const uint64_t dQt = smem_desc_mnmajor(smem_u32(sQ), SH::ROWB, SH::QBOX);
         const uint32_t tbase = __shfl_sync(0xffffffffu, tmem, 0) + 128;
         int stage = 0, n = 0, it = 0;
         bool alive = true;
-        int nx = (int)blockIdx.x < n_q ? a.l.rows[blockIdx.x].ncols : 0;
-        for (int t = blockIdx.x; t < n_q && alive; t += step) {
+        int nx = t0 < n_q ? a.l.rows[t0].ncols : 0;
+        for (int t = t0; t < n_q && alive; t += step) {
             const int nt = __shfl_sync(0xffffffffu, (nx + 127) >> 7, 0);
             if (t + step < n_q) nx = a.l.rows[t + step].ncols;
             if (nt == 0) continue;
@@ -447,10 +478,25 @@ __global__ void __launch_bounds__(list_threads(BWD), 1)
                     for (int kk = 0; kk < 8; ++kk)   // 16 keys each
                         tc_mma(tbase + qb * 64, ad + kk * SH::ROWB, bd + kk * 128, idQ, kk > 0 || i > 0 ? 1u : 0u);
                     tc_commit(&kempty[stage]);
-                    tc_commit(&gfree[b]);
+                    if (!ROWS) tc_commit(&gfree[b]);
                     if (i == nt - 1) tc_commit(&dqfull[qb]);
                 }
                 __syncwarp();
+                if constexpr (ROWS) {   // the tile's rows of dK: G [keys x heads] . Q [heads x d]
+                    alive = tc_wait_warp(&dkfree[b], ((n >> 1) & 1) ^ 1u, status, 35, abort_flag, alive);
+                    if (!alive) break;
+                    tc_fence_after();
+                    const uint64_t gd = dGk + b * (SH::GTILE >> 4), qd = dQt + qb * (SH::QTILE >> 4);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < HP / 16; ++kk)
+                            tc_mma(tbase + 128 + b * 128, gd + kk * 2, qd + kk * SH::ROWB, idK, kk > 0 ? 1u : 0u);
+                        tc_commit(&gfree[b]);
+                        tc_commit(&dkfull[b]);
+                        if (i == nt - 1) tc_commit(&qempty[qb]);
+                    }
+                    __syncwarp();
+                }
                 if (++stage == n_stages) stage = 0;
             }
             ++it;
@@ -459,6 +505,54 @@ __global__ void __launch_bounds__(list_threads(BWD), 1)
         __syncwarp();
         mbar_wait(&drain[1], 0, status, 34);
         __syncwarp();
+    } else if (ROWS && warp >= 6 + kEpi) {
+        // ------------------------------------------------- rows of dK to memory
+        const int quarter = warp & 3, lrow = quarter * 32 + lane;
+        int n = 0;
+        bool alive = true;
+        RowDesc nx = t0 < n_q ? a.l.rows[t0] : none;
+        for (int t = t0; t < n_q && alive; t += step) {
+            const RowDesc r = nx;
+            const int nt = (r.ncols + 127) >> 7;
+            if (t + step < n_q) nx = a.l.rows[t + step];
+            const int32_t* l = a.l.lists + (int64_t)t * k;
+            const int kb = a.l.k_off[r.seq];
+            const int64_t word = (int64_t)((t - a.t0) >> 5) * a.l.n_k;
+            const uint32_t below = (1u << ((t - a.t0) & 31)) - 1u;
+            // the next tile's place is looked up while this one is stored: key two tiles ahead
+            auto key_row = [&](int i) {
+                const int j = i * 128 + lrow;
+                const int s = kb + (j < r.ncols ? __ldg(l + j) : 0);
+                return DSA_CHECK(s >= 0 && s < a.l.n_k, status, 118) ? s : 0;
+            };
+            auto place = [&](int s) {
+                return (int64_t)__ldg(a.base + s / kPosBlock) + __ldg(a.off + s) + __ldg(a.pre + word + s) +
+                       __popc(__ldg(a.bits + word + s) & below);
+            };
+            int64_t at = nt > 0 ? place(key_row(0)) : 0;
+            int s_next = nt > 1 ? key_row(1) : 0;
+            for (int i = 0; i < nt && alive; ++i, ++n) {
+                const int b = n & 1, j = i * 128 + lrow;
+                float* out = a.part + at * D;
+                if (i + 1 < nt) at = place(s_next);
+                if (i + 2 < nt) s_next = key_row(i + 2);
+                alive = tc_wait_warp(&dkfull[b], (n >> 1) & 1, status, 36, abort_flag, alive);
+                if (!alive) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    float v[32];
+                    tmem_load<32>(tmem + 256 + b * 128 + c + ((uint32_t)(quarter * 32) << 16), v);
+                    if (j < r.ncols) {
+#pragma unroll
+                        for (int x = 0; x < 32; x += 8) store_f32x8(out + c + x, v + x);
+                    }
+                    __syncwarp();
+                }
+                tc_fence_before();
+                mbar_arrive(&dkfree[b]);
+            }
+        }
     } else {
         // ---------------------------------------------------------- epilogue
         // Named barriers are met by all threads of a set whatever an abort makes of the waits, so the
@@ -470,9 +564,9 @@ __global__ void __launch_bounds__(list_threads(BWD), 1)
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         int n = 0, it = 0, all = 0;
         bool alive = true;
-        RowDesc nx = (int)blockIdx.x < n_q ? a.l.rows[blockIdx.x] : none;
-        float wnext = st < H && (int)blockIdx.x < n_q ? a.l.W[(int64_t)blockIdx.x * H + st] : 0.f;
-        for (int t = blockIdx.x; t < n_q; t += step, ++all) {
+        RowDesc nx = t0 < n_q ? a.l.rows[t0] : none;
+        float wnext = st < H && t0 < n_q ? a.l.W[(int64_t)t0 * H + st] : 0.f;
+        for (int t = t0; t < n_q; t += step, ++all) {
             const RowDesc r = nx;
             float* w = sW + (set * 2 + (all & 1)) * HP;
             if (st < HP) w[st] = wnext;
@@ -600,7 +694,7 @@ __global__ void __launch_bounds__(list_threads(BWD), 1)
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 256);
+        tmem_dealloc(tmem, kCols);
     }
 }
 

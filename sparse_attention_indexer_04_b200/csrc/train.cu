@@ -8,6 +8,7 @@
 #include "../../include/dsa_index.h"
 #include "distill.cuh"
 #include "host.cuh"
+#include "list_dk_rows.cuh"
 #include "list_dk_tc.cuh"
 #include "list_tc.cuh"
 #include "norm.cuh"
@@ -159,7 +160,35 @@ struct ListPlan {
     int32_t key_blocks; // of the longest sequence
     int32_t units;      // key blocks over all sequences (an upper bound)
     int32_t parts;
+    bool by_rows;       // dK from the dQ pass's rows (list_dk_rows.cuh), not from dense key blocks
+    int32_t chunk;      // by_rows: queries of one launch
+    int32_t words;      // by_rows: 32-query words of a launch
+    uint32_t* bits;     // by_rows: where each key's rows lie (list_dk_rows.cuh)
+    uint16_t* pre;
+    uint32_t *count, *off, *base;
+    float* acc;         // by_rows, more than one launch: sums so far
 };
+
+// Bytes of dK rows kept between two launches: 888 queries of 2048 places at d = 128, six a CTA.
+constexpr size_t kRowsBudget = size_t(1024) << 20;
+
+// Whether dK is summed from one row per listed pair or from dense products over whole key blocks.
+// Measured at H = 64, d = 128: a row costs 0.17 ns (written and read once), a (query, block) product
+// 7.3 ns and in proportion to H, so rows pay below 40 * H / 64 listed places per visited block.  The
+// host knows places and blocks of whole sequences; a causal prefix is half of that on average over a
+// training batch and all of it for a chunk of queries at the end, hence the factor of 1.4 between.
+bool dk_by_rows(const dsa_batch* b, int32_t k)
+{
+    double places = 0, blocks = 0;
+    for (int i = 0; i < b->num_seqs; ++i) {
+        const double nq = b->q_offsets_host[i + 1] - b->q_offsets_host[i];
+        const int32_t L = b->k_offsets_host[i + 1] - b->k_offsets_host[i];
+        const int32_t listed = std::min(k, L);
+        places += nq * listed;
+        blocks += nq * std::min(listed, (L + kDkKeys - 1) / kDkKeys);
+    }
+    return places < blocks * 28.0 * b->num_heads / 64.0;
+}
 
 // CTAs that share a key block's queries: enough for three waves over the GPU (a block's work is its
 // queries', so early blocks of a causal sequence have the most), no more than there are groups of 16
@@ -171,15 +200,30 @@ int32_t dk_parts(int32_t units, int32_t max_q)
     return std::max((max_q + kDkMaxList - 1) / kDkMaxList, std::max(1, std::min(fill, most)));
 }
 
-size_t list_plan(char* base, const dsa_batch* b, const HostInfo& hi, bool backward, ListPlan* p)
+size_t list_plan(char* base, const dsa_batch* b, const HostInfo& hi, int32_t k, bool backward, ListPlan* p)
 {
     Carver c{base};
     *p = ListPlan{};
     p->rows = c.take<RowDesc>(std::max(1, b->num_queries));
     if (!backward) return c.off;
+    p->by_rows = dk_by_rows(b, k);
     p->key_blocks = (hi.max_k + kDkKeys - 1) / kDkKeys;
     p->units = b->num_keys / kDkKeys + b->num_seqs;
     p->parts = dk_parts(p->units, hi.max_q);
+    if (p->by_rows) {
+        const int64_t row = std::min(k, std::max(1, hi.max_k));   // places of a query at most
+        const int64_t fit = int64_t(kRowsBudget / (size_t(row) * b->head_dim * 4));
+        p->chunk = (int32_t)std::min<int64_t>(b->num_queries, fit > 148 ? fit / 148 * 148 : std::max<int64_t>(1, fit));
+        p->words = (p->chunk + 31) / 32;
+        p->part = c.take<float>(size_t(p->chunk) * row * b->head_dim);
+        p->bits = c.take<uint32_t>(size_t(p->words) * b->num_keys);
+        p->pre = c.take<uint16_t>(size_t(p->words) * b->num_keys);
+        p->count = c.take<uint32_t>(b->num_keys);
+        p->off = c.take<uint32_t>(b->num_keys);
+        p->base = c.take<uint32_t>((b->num_keys + kPosBlock - 1) / kPosBlock);
+        if (p->chunk < b->num_queries) p->acc = c.take<float>(size_t(b->num_keys) * b->head_dim);
+        return c.off;
+    }
     p->edge = c.take<uint16_t>(size_t(p->key_blocks + 1) * std::max(1, b->num_queries));
     if (p->parts > 1) p->part = c.take<float>(size_t(p->parts) * b->num_keys * b->head_dim);
     return c.off;
@@ -212,45 +256,49 @@ ListArgs list_args(const dsa_batch* b, const void* Q, const void* K, const float
     return a;
 }
 
-dsa_status list_rows(const dsa_batch* b, int32_t k, const int32_t* lists, const ListPlan& p, void* ws, cudaStream_t st)
+// The usable lists; with edges also the list places at the borders of the key blocks.
+dsa_status list_rows(const dsa_batch* b, int32_t k, const int32_t* lists, const ListPlan& p, bool edges, void* ws,
+                     cudaStream_t st)
 {
     dsa_status s = clear_status(ws, st);
     if (s != DSA_OK || b->num_queries == 0) return s;
+    const int32_t quads = k % 4 == 0 && (reinterpret_cast<uintptr_t>(lists) & 15) == 0;
     DSA_LAUNCH(kProfSetup, st, list_rows_kernel<<<(b->num_queries + 7) / 8, 256, 0, st>>>(
-        lists, k, b->q_offsets, b->k_offsets, b->q_pos, b->num_seqs, b->num_queries, p.rows,
-        static_cast<uint32_t*>(ws)));
+        lists, k, quads, b->q_offsets, b->k_offsets, b->q_pos, b->num_seqs, b->num_queries, p.rows,
+        edges ? p.edge : nullptr, p.key_blocks, static_cast<uint32_t*>(ws)));
     return launched();
 }
 
 constexpr int kSmemMax = 232448;   // dynamic shared memory of one CTA
 
-template <int D, int HP, bool BWD>
-dsa_status list_tc_launch(const ListArgs& l, cudaStream_t st)
+template <int D, int HP, int MODE>
+dsa_status list_tc_launch(const ListArgs& l, int32_t t0, int32_t t1, const ListPlan& p, cudaStream_t st)
 {
     using SH = ListShape<D, HP>;
     CUtensorMap mq;
     if (!make_tile_map(&mq, l.Q, int64_t(l.n_q) * l.H, D, l.H)) return DSA_ERR_CUDA;
-    ListTcArgs a{l, std::min(8, int((kSmemMax - SH::bytes(0)) / SH::KTILE))};
+    const ListTcArgs a{l, std::min(8, int((kSmemMax - SH::bytes(0)) / SH::KTILE)), t0, t1,
+                       p.part, p.bits, p.pre, p.off, p.base};
     const int smem = std::max<int>(SH::bytes(a.n_stages), 120 * 1024);   // one CTA an SM
-    dsa_status s = set_smem(list_tc_kernel<D, HP, BWD>, smem);
+    dsa_status s = set_smem(list_tc_kernel<D, HP, MODE>, smem);
     if (s != DSA_OK) return s;
-    DSA_LAUNCH(BWD ? kProfListDq : kProfListScores, st,
-               launch_pdl(true, list_tc_kernel<D, HP, BWD>, std::min(l.n_q, 148), list_threads(BWD), smem, st, mq, a));
+    DSA_LAUNCH(MODE ? kProfListDq : kProfListScores, st,
+               launch_pdl(true, list_tc_kernel<D, HP, MODE>, std::min(t1 - t0, 148), list_threads(MODE), smem, st, mq, a));
     return launched();
 }
 
-template <int D, bool BWD>
-dsa_status list_tc(const ListArgs& a, cudaStream_t st)
+template <int D, int MODE>
+dsa_status list_tc(const ListArgs& a, int32_t t0, int32_t t1, const ListPlan& p, cudaStream_t st)
 {
-    if (a.H <= 16) return list_tc_launch<D, 16, BWD>(a, st);
-    if (a.H <= 32) return list_tc_launch<D, 32, BWD>(a, st);
-    return list_tc_launch<D, 64, BWD>(a, st);
+    if (a.H <= 16) return list_tc_launch<D, 16, MODE>(a, t0, t1, p, st);
+    if (a.H <= 32) return list_tc_launch<D, 32, MODE>(a, t0, t1, p, st);
+    return list_tc_launch<D, 64, MODE>(a, t0, t1, p, st);
 }
 
 template <int D>
-dsa_status list_scores_d(const ListArgs& a, cudaStream_t st)
+dsa_status list_scores_d(const ListArgs& a, const ListPlan& p, cudaStream_t st)
 {
-    return list_tc<D, false>(a, st);
+    return list_tc<D, kListScores>(a, 0, a.n_q, p, st);
 }
 
 template <int D, int H>
@@ -289,14 +337,30 @@ template <int D>
 dsa_status list_backward_d(const ListArgs& a, const ListPlan& p, cudaStream_t st)
 {
     dsa_status s;
-    if (a.n_q > 0 && (a.dQ || a.dW) && (s = list_tc<D, true>(a, st)) != DSA_OK) return s;
-    if (a.n_k == 0 || !a.dK) return DSA_OK;
+    const bool want_k = a.n_k > 0 && a.dK;
     if (a.n_q == 0)   // nothing lists a key
-        return cudaMemsetAsync(a.dK, 0, size_t(a.n_k) * D * 2, st) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
-    DSA_LAUNCH(kProfSetup, st, list_edges_kernel<<<(a.n_q + 7) / 8, 256, 0, st>>>(a.lists, a.k, a.rows, a.n_q,
-                                                                                  p.key_blocks, p.edge));
-    if ((s = launched()) != DSA_OK) return s;
-    return list_dk<D>(a, p, st);
+        return !want_k || cudaMemsetAsync(a.dK, 0, size_t(a.n_k) * D * 2, st) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+    if (!want_k || !p.by_rows) {
+        if ((a.dQ || a.dW) && (s = list_tc<D, kListGrad>(a, 0, a.n_q, p, st)) != DSA_OK) return s;
+        return want_k ? list_dk<D>(a, p, st) : DSA_OK;
+    }
+    for (int32_t t0 = 0; t0 < a.n_q; t0 += p.chunk) {
+        const int32_t t1 = std::min(t0 + p.chunk, a.n_q), words = (t1 - t0 + 31) / 32;
+        const int32_t blocks = (a.n_k + kPosBlock - 1) / kPosBlock;
+        if (cudaMemsetAsync(p.bits, 0, size_t(words) * a.n_k * 4, st) != cudaSuccess) return DSA_ERR_CUDA;
+        DSA_LAUNCH(kProfSetup, st, list_bits_kernel<<<(t1 - t0 + 7) / 8, 256, 0, st>>>(a.lists, a.k, a.rows, a.k_off, t0, t1,
+                                                                                       a.n_k, p.bits, a.status));
+        DSA_LAUNCH(kProfSetup, st, list_count_kernel<<<blocks, kPosBlock, 0, st>>>(p.bits, words, a.n_k, p.pre, p.count,
+                                                                                  p.off, p.base));
+        DSA_LAUNCH(kProfSetup, st, list_base_kernel<<<1, 1024, 0, st>>>(p.base, blocks));
+        if ((s = launched()) != DSA_OK) return s;
+        if ((s = list_tc<D, kListGradRows>(a, t0, t1, p, st)) != DSA_OK) return s;
+        const DkRowsArgs r{p.part, p.count, p.off, p.base, p.acc, a.dK, a.n_k, t0 == 0, t1 == a.n_q};
+        DSA_LAUNCH(kProfListDk, st, list_dk_rows_kernel<D>
+                   <<<(a.n_k + kRowsWarps - 1) / kRowsWarps, kRowsWarps * 32, 0, st>>>(r));
+        if ((s = launched()) != DSA_OK) return s;
+    }
+    return DSA_OK;
 }
 
 }  // namespace
@@ -416,7 +480,7 @@ size_t dsa_list_scores_workspace(const dsa_batch* b, int32_t k)
 {
     HostInfo hi;
     ListPlan p;
-    return list_check(b, &hi, k) == DSA_OK ? list_plan(nullptr, b, hi, false, &p) : 0;
+    return list_check(b, &hi, k) == DSA_OK ? list_plan(nullptr, b, hi, k, false, &p) : 0;
 }
 
 dsa_status dsa_list_scores(const dsa_batch* b, const void* Q, const void* K, const float* W, int32_t k,
@@ -429,16 +493,16 @@ dsa_status dsa_list_scores(const dsa_batch* b, const void* Q, const void* K, con
     if (b->num_queries > 0 && (!lists || !scores)) return DSA_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(lists) | reinterpret_cast<uintptr_t>(scores)) & 3) return DSA_ERR_INVALID_ARG;
     ListPlan p;
-    if ((s = check_ws(ws, ws_bytes, list_plan(nullptr, b, hi, false, &p))) != DSA_OK) return s;
-    list_plan(static_cast<char*>(ws), b, hi, false, &p);
+    if ((s = check_ws(ws, ws_bytes, list_plan(nullptr, b, hi, k, false, &p))) != DSA_OK) return s;
+    list_plan(static_cast<char*>(ws), b, hi, k, false, &p);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if ((s = list_rows(b, k, lists, p, ws, st)) != DSA_OK || b->num_queries == 0) return s;
+    if ((s = list_rows(b, k, lists, p, false, ws, st)) != DSA_OK || b->num_queries == 0) return s;
     ListArgs a = list_args(b, Q, K, W, k, lists, p, ws);
     a.scores = scores;
     switch (b->head_dim) {
-    case 32: return list_scores_d<32>(a, st);
-    case 64: return list_scores_d<64>(a, st);
-    default: return list_scores_d<128>(a, st);
+    case 32: return list_scores_d<32>(a, p, st);
+    case 64: return list_scores_d<64>(a, p, st);
+    default: return list_scores_d<128>(a, p, st);
     }
 }
 
@@ -446,7 +510,7 @@ size_t dsa_list_scores_backward_workspace(const dsa_batch* b, int32_t k)
 {
     HostInfo hi;
     ListPlan p;
-    return list_check(b, &hi, k) == DSA_OK ? list_plan(nullptr, b, hi, true, &p) : 0;
+    return list_check(b, &hi, k) == DSA_OK ? list_plan(nullptr, b, hi, k, true, &p) : 0;
 }
 
 dsa_status dsa_list_scores_backward(const dsa_batch* b, const void* Q, const void* K, const float* W, int32_t k,
@@ -462,10 +526,10 @@ dsa_status dsa_list_scores_backward(const dsa_batch* b, const void* Q, const voi
         return DSA_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(dQ) | reinterpret_cast<uintptr_t>(dK)) & 15) return DSA_ERR_INVALID_ARG;
     ListPlan p;
-    if ((s = check_ws(ws, ws_bytes, list_plan(nullptr, b, hi, true, &p))) != DSA_OK) return s;
-    list_plan(static_cast<char*>(ws), b, hi, true, &p);
+    if ((s = check_ws(ws, ws_bytes, list_plan(nullptr, b, hi, k, true, &p))) != DSA_OK) return s;
+    list_plan(static_cast<char*>(ws), b, hi, k, true, &p);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if ((s = list_rows(b, k, lists, p, ws, st)) != DSA_OK) return s;
+    if ((s = list_rows(b, k, lists, p, dK != nullptr && !p.by_rows, ws, st)) != DSA_OK) return s;
     ListArgs a = list_args(b, Q, K, W, k, lists, p, ws);
     a.ds = dscores;
     a.dQ = static_cast<__nv_bfloat16*>(dQ);

@@ -282,6 +282,23 @@ def test_list_scores_tile_edges(k):
     check_lists(b, random_lists(g, b, k), randn(g, b.n_q, k) * 1e-3)
 
 
+@pytest.mark.parametrize("H,d", [(64, 128), (64, 64), (32, 32), (16, 128), (8, 64), (1, 32)])
+def test_list_scores_sparse_lists(H, d):
+    """Lists that cover little of their prefix (a few places per block of 256 keys, dK then comes from one row per
+    listed pair), empty blocks between them, sequences that begin inside a block of key rows."""
+    b = workloads.ragged(H * 3 + d, [37, 0, 90, 3], [5000, 300, 7001, 20], H=H, d=d, k=8, integer=False)
+    g = gen(H + d)
+    for k in (4, 133):
+        check_lists(b, random_lists(g, b, k), randn(g, b.n_q, k))
+
+
+def test_list_scores_sparse_lists_in_several_launches():
+    """More listed pairs than one launch's rows hold (1 GiB): the sums carry over."""
+    b = workloads.ragged(5, [1400], [40000], H=64, d=128, k=1500, integer=False)
+    g = gen(6)
+    check_lists(b, random_lists(g, b, 1500), randn(g, b.n_q, 1500))
+
+
 def test_list_scores_integers_are_exact():
     """Integer keys and queries, power-of-two weights and gradients: every sum is exact in fp32, zeros of the
     products included, so results are the 64-bit ones rounded once."""
