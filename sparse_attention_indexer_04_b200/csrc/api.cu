@@ -949,6 +949,32 @@ dsa_status hisa_one_pass(const dsa_batch* b, const HostInfo& hi, const void* Q, 
 
 }  // namespace
 
+namespace dsa {
+
+int64_t dense_scores_ld(int32_t max_k) { return score_ld(max_k); }
+
+size_t dense_scores_plan_bytes(const dsa_batch* b, const HostInfo& hi)
+{
+    DensePlan p;
+    return dense_plan(nullptr, b, hi, 0, &p);
+}
+
+dsa_status dense_scores(const dsa_batch* b, const HostInfo& hi, const void* Q, const void* K, const float* W, float* S,
+                        char* plan, uint32_t* status, cudaStream_t st)
+{
+    DensePlan p;
+    dense_plan(plan, b, hi, 0, &p);
+    DSA_LAUNCH(kProfSetup, st, dense_rows_kernel<<<(b->num_queries + 255) / 256, 256, 0, st>>>(
+        b->q_offsets, b->k_offsets, b->q_pos, b->num_seqs, b->num_queries, p.rows));
+    dsa_status s = launched();
+    if (s != DSA_OK) return s;
+    const TcSource src{Q, b->num_queries, W, b->q_offsets, b->q_offsets_host, b->num_seqs};
+    return tc_score(p.rows, b->num_queries, 0, src, b->num_heads, b->head_dim, K, b->num_keys, b->k_offsets, ColMap{},
+                    hi.max_k, S, score_ld(hi.max_k), p.units, p.tile_base, status, st);
+}
+
+}  // namespace dsa
+
 // =====================================================================
 extern "C" {
 

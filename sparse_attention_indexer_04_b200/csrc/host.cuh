@@ -234,4 +234,12 @@ inline dsa_status clear_status(void* ws, cudaStream_t st)
     return cudaMemsetAsync(ws, 0, kHeaderBytes, st) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
+// Scores of every eligible key in one tensor-core launch, without filling the others (api.cu):
+// S [n_q][dense_scores_ld] fp32; plan: dense_scores_plan_bytes of workspace, 256-byte aligned; status: the
+// call's status word.
+int64_t dense_scores_ld(int32_t max_k);
+size_t dense_scores_plan_bytes(const dsa_batch* b, const HostInfo& hi);
+dsa_status dense_scores(const dsa_batch* b, const HostInfo& hi, const void* Q, const void* K, const float* W, float* S,
+                        char* plan, uint32_t* status, cudaStream_t st);
+
 }  // namespace dsa

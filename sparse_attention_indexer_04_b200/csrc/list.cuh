@@ -114,4 +114,60 @@ __global__ void __launch_bounds__(256) list_rows_kernel(const int32_t* lists, in
     for (int b = last + lane; b <= n_blocks; b += 32) edge[(int64_t)b * n_q + t] = (uint16_t)n;
 }
 
+// scores[t][j] = S[t][lists[t][j]] for the usable places (as list_rows_kernel finds them), -inf in the others;
+// S [n_q][ld] holds every eligible score.  One warp per query, `quads`: four places a lane.
+template <int PER>
+__global__ void __launch_bounds__(256) list_pick_kernel(const int32_t* lists, int32_t k, const int32_t* q_off,
+                                                        const int32_t* k_off, const int32_t* q_pos, int32_t n_seqs,
+                                                        int32_t n_q, const float* S, int64_t ld, float* scores,
+                                                        uint32_t* status)
+{
+    const int t = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (t >= n_q) return;
+    const int seq = find_seq(q_off, n_seqs, t);
+    const int L = k_off[seq + 1] - k_off[seq];
+    const int lim = eligible_count(q_pos[t], L);
+    const int32_t* l = lists + (int64_t)t * k;
+    const float* row = S + (int64_t)t * ld;
+    float* out = scores + (int64_t)t * k;
+    int stop = k, carry = -1;
+    bool bad = false;
+    int v[PER], next[PER];
+    auto read = [&](int i) {
+        if constexpr (PER == 4) {
+            const int4 x = i < k ? __ldg(reinterpret_cast<const int4*>(l + i)) : make_int4(-1, -1, -1, -1);
+            next[0] = x.x; next[1] = x.y; next[2] = x.z; next[3] = x.w;
+        } else {
+            next[0] = i < k ? __ldg(l + i) : -1;
+        }
+    };
+    read(PER * lane);
+    for (int i0 = 0; i0 < k; i0 += 32 * PER) {
+        const int i = i0 + PER * lane;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) v[e] = next[e];
+        read(i + 32 * PER);
+        const int up = __shfl_up_sync(0xffffffffu, v[PER - 1], 1);
+        int prev = lane == 0 ? carry : up, mine = k;
+        carry = __shfl_sync(0xffffffffu, v[PER - 1], 31);
+#pragma unroll
+        for (int e = PER - 1; e >= 0; --e) {
+            const int before = e > 0 ? v[e - 1] : prev;
+            const bool wrong = v[e] >= 0 && (v[e] >= L || (i + e > 0 && (before < 0 || before >= v[e])));
+            bad |= wrong && i + e < k;
+            if (v[e] < 0 || wrong || v[e] >= lim) mine = min(mine, i + e);
+        }
+        stop = min(stop, (int)__reduce_min_sync(0xffffffffu, (unsigned)mine));
+        float s[PER];
+#pragma unroll
+        for (int e = 0; e < PER; ++e)
+            s[e] = i + e < stop && DSA_CHECK(v[e] >= 0 && v[e] < lim, status, 119) ? __ldg(row + v[e]) : __int_as_float(0xff800000);
+        if (i < k) {
+            if constexpr (PER == 4) *reinterpret_cast<float4*>(out + i) = make_float4(s[0], s[1], s[2], s[3]);
+            else out[i] = s[0];
+        }
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(status, kErrBadRow, (uint32_t)t);
+}
+
 }  // namespace dsa

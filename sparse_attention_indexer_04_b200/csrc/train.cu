@@ -160,6 +160,9 @@ struct ListPlan {
     int32_t key_blocks; // of the longest sequence
     int32_t units;      // key blocks over all sequences (an upper bound)
     int32_t parts;
+    float* S;           // forward, by picking: every eligible score
+    char* dense;        // and its launch's plan
+    bool picking;
     bool by_rows;       // dK from the dQ pass's rows (list_dk_rows.cuh), not from dense key blocks
     int32_t chunk;      // by_rows: queries of one launch
     int32_t words;      // by_rows: 32-query words of a launch
@@ -172,22 +175,49 @@ struct ListPlan {
 // Bytes of dK rows kept between two launches: 888 queries of 2048 places at d = 128, six a CTA.
 constexpr size_t kRowsBudget = size_t(1024) << 20;
 
+// What a batch's lists hold, as far as the host knows: the queries of a sequence taken as its last ones
+// (a training batch: all of them; a chunk at the end of a context).
+struct ListWork {
+    double listed = 0;   // listed (query, key) pairs
+    double dense = 0;    // eligible pairs
+    double blocks = 0;   // (query, key block) pairs with a listed key
+};
+
+ListWork list_work(const dsa_batch* b, int32_t k)
+{
+    ListWork w;
+    for (int i = 0; i < b->num_seqs; ++i) {
+        const double L = b->k_offsets_host[i + 1] - b->k_offsets_host[i];
+        const double nq = std::min<double>(b->q_offsets_host[i + 1] - b->q_offsets_host[i], L);
+        const double p0 = L - nq + 1, p1 = L;   // prefix lengths from p0 to p1
+        // sums over p0 .. p1 of p, of min(k, p) and of the blocks they touch
+        const auto sum = [](double lo, double hi) { return hi < lo ? 0. : (lo + hi) * (hi - lo + 1) / 2; };
+        const double m = std::min<double>(k, p1), dense = sum(p0, p1);
+        const double listed = sum(p0, std::min(m, p1)) + std::max(0., p1 - std::max(p0 - 1, m)) * k;
+        w.dense += dense;
+        w.listed += listed;
+        w.blocks += std::min(listed, dense / kDkKeys + nq / 2);
+    }
+    return w;
+}
+
 // Whether dK is summed from one row per listed pair or from dense products over whole key blocks.
-// Measured at H = 64, d = 128: a row costs 0.17 ns (written and read once), a (query, block) product
-// 7.3 ns and in proportion to H, so rows pay below 40 * H / 64 listed places per visited block.  The
-// host knows places and blocks of whole sequences; a causal prefix is half of that on average over a
-// training batch and all of it for a chunk of queries at the end, hence the factor of 1.4 between.
+// Measured at d = 128: a row 0.22 ns (written by the dQ pass, read once), a (query, block) product 6.8 ns
+// with 64 heads, 2.5 with 8, 1.2 with 4.
 bool dk_by_rows(const dsa_batch* b, int32_t k)
 {
-    double places = 0, blocks = 0;
-    for (int i = 0; i < b->num_seqs; ++i) {
-        const double nq = b->q_offsets_host[i + 1] - b->q_offsets_host[i];
-        const int32_t L = b->k_offsets_host[i + 1] - b->k_offsets_host[i];
-        const int32_t listed = std::min(k, L);
-        places += nq * listed;
-        blocks += nq * std::min(listed, (L + kDkKeys - 1) / kDkKeys);
-    }
-    return places < blocks * 28.0 * b->num_heads / 64.0;
+    const ListWork w = list_work(b, k);
+    return w.listed * 0.22 < w.blocks * (1.2 + 5.6 * b->num_heads / 64.);
+}
+
+// Whether the listed scores are picked from all scores of the prefix or computed from gathered keys.
+// Measured at d = 128: a gathered pair 33 ps, a dense one 14 ps with 64 heads, and 2 ps to write and read it.
+bool scores_by_picking(const dsa_batch* b, const HostInfo& hi, int32_t k)
+{
+    if (size_t(b->num_queries) * dense_scores_ld(hi.max_k) * 4 > (size_t(4) << 30)) return false;
+    const ListWork w = list_work(b, k);
+    const double d = b->head_dim / 128.;
+    return w.dense * (2 + 14 * d * b->num_heads / 64.) < w.listed * 33 * d;
 }
 
 // CTAs that share a key block's queries: enough for three waves over the GPU (a block's work is its
@@ -204,6 +234,12 @@ size_t list_plan(char* base, const dsa_batch* b, const HostInfo& hi, int32_t k, 
 {
     Carver c{base};
     *p = ListPlan{};
+    p->picking = !backward && scores_by_picking(b, hi, k);
+    if (p->picking) {
+        p->S = c.take<float>(size_t(b->num_queries) * dense_scores_ld(hi.max_k));
+        p->dense = c.take<char>(dense_scores_plan_bytes(b, hi));
+        return c.off;
+    }
     p->rows = c.take<RowDesc>(std::max(1, b->num_queries));
     if (!backward) return c.off;
     p->by_rows = dk_by_rows(b, k);
@@ -496,6 +532,17 @@ dsa_status dsa_list_scores(const dsa_batch* b, const void* Q, const void* K, con
     if ((s = check_ws(ws, ws_bytes, list_plan(nullptr, b, hi, k, false, &p))) != DSA_OK) return s;
     list_plan(static_cast<char*>(ws), b, hi, k, false, &p);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (p.picking) {
+        uint32_t* status = static_cast<uint32_t*>(ws);
+        if ((s = clear_status(ws, st)) != DSA_OK) return s;
+        if ((s = dense_scores(b, hi, Q, K, W, p.S, p.dense, status, st)) != DSA_OK) return s;
+        const bool quads = k % 4 == 0 && ((reinterpret_cast<uintptr_t>(lists) | reinterpret_cast<uintptr_t>(scores)) & 15) == 0;
+        const auto pick = quads ? list_pick_kernel<4> : list_pick_kernel<1>;
+        DSA_LAUNCH(kProfListScores, st, pick<<<(b->num_queries + 7) / 8, 256, 0, st>>>(
+            lists, k, b->q_offsets, b->k_offsets, b->q_pos, b->num_seqs, b->num_queries, p.S, dense_scores_ld(hi.max_k),
+            scores, status));
+        return launched();
+    }
     if ((s = list_rows(b, k, lists, p, false, ws, st)) != DSA_OK || b->num_queries == 0) return s;
     ListArgs a = list_args(b, Q, K, W, k, lists, p, ws);
     a.scores = scores;
