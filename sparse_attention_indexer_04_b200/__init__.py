@@ -425,7 +425,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, out_dtype
     n, d = x.shape
     w, b = _dense(weight, "weight", dev, (d,), torch.float32), _dense(bias, "bias", dev, (d,), torch.float32)
     if out is None:
-        out = torch.empty((n, d), dtype=out_dtype or x.dtype, device=x.device)
+        out = x.new_empty((n, d), dtype=out_dtype)
     ld_y = _rows(out, "out", dev, n, d)
     mean = rstd = mp = rp = None
     if want_stats:
@@ -452,7 +452,8 @@ def layer_norm_backward(dy, x, weight, mean, rstd, dx=None, ws=None, stream=None
         dx = x.new_empty((n, d))
     ld_dx = _rows(dx, "dx", dev, n, d, x.dtype)
     dw, db = x.new_empty(d, dtype=torch.float32), x.new_empty(d, dtype=torch.float32)
-    ws = _workspace(layer_norm_backward_workspace(n, d), x.device, ws)
+    if ws is None:
+        ws = _workspace(layer_norm_backward_workspace(n, d), x.device)
     _check(_on(dev, _lib.dsa_layer_norm_backward, n, d, dy.data_ptr(), _TYPES[dy.dtype], ld_dy, x.data_ptr(),
                _TYPES[x.dtype], ld_x, w, mp, rp, dx.data_ptr(), ld_dx, dw.data_ptr(), db.data_ptr(), ws.data_ptr(),
                ws.numel() * ws.element_size(), stream=stream), "dsa_layer_norm_backward")
@@ -506,7 +507,8 @@ def list_scores(layout: Layout, Q, K, W, lists, scores=None, ws=None, stream=Non
     dev, k, q, kk, w, l = _list_inputs(layout, Q, K, W, lists)
     if scores is None:
         scores = W.new_empty(lists.shape)
-    ws = _workspace(list_scores_workspace(layout, k), Q.device, ws)
+    if ws is None:
+        ws = _workspace(list_scores_workspace(layout, k), Q.device)
     _check(_on(dev, _lib.dsa_list_scores, layout.ref(), q, kk, w, k, l,
                _dense(scores, "scores", dev, lists.shape, torch.float32), ws.data_ptr(), ws.numel() * ws.element_size(),
                stream=stream), "dsa_list_scores")
@@ -525,7 +527,8 @@ def list_scores_backward(layout: Layout, Q, K, W, lists, dscores, dQ=None, dK=No
     dQ = torch.empty_like(Q) if dQ is None else dQ
     dK = torch.empty_like(K) if dK is None else dK
     dW = torch.empty_like(W) if dW is None else dW
-    ws = _workspace(list_scores_backward_workspace(layout, k), Q.device, ws)
+    if ws is None:
+        ws = _workspace(list_scores_backward_workspace(layout, k), Q.device)
     _check(_on(dev, _lib.dsa_list_scores_backward, layout.ref(), q, kk, w, k, l, ds,
                _dense(dQ, "dQ", dev, Q.shape, torch.bfloat16), _dense(dK, "dK", dev, K.shape, torch.bfloat16),
                _dense(dW, "dW", dev, W.shape, torch.float32), ws.data_ptr(), ws.numel() * ws.element_size(),
