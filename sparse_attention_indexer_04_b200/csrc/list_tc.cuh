@@ -29,7 +29,7 @@ constexpr int kListTcProducers = 4;
 constexpr int list_sets(int mode) { return mode ? 4 : 2; }
 constexpr int list_threads(int mode)
 {
-    return 32 * (1 + kListTcProducers + (mode ? 1 : 0) + (mode == 2 ? 4 : 0)) + 128 * list_sets(mode);
+    return 32 * (1 + kListTcProducers + (mode ? 1 : 0) + (mode == 2 ? 8 : 0)) + 128 * list_sets(mode);
 }
 constexpr uint32_t kErrListAlign = 3;
 
@@ -197,8 +197,8 @@ struct ListShape {
     static constexpr uint32_t g_off(int stages) { return q_off(stages) + align1k(2 * QTILE); }
     static constexpr uint32_t w_off(int stages) { return g_off(stages) + 2 * GTILE; }
     static constexpr uint32_t x_off(int stages) { return w_off(stages) + W_BYTES + DW_BYTES + BAR_BYTES; }
-    // rows: 4 KB a writing warp, a 32 x 32 tile of dK on its way to memory
-    static constexpr uint32_t bytes(int stages, bool rows) { return x_off(stages) + (rows ? 4u * 4096u : 0u); }
+    // rows: 4 KB a writing warp (eight), a 32 x 32 tile of dK on its way to memory
+    static constexpr uint32_t bytes(int stages, bool rows) { return x_off(stages) + (rows ? 8u * 4096u : 0u); }
 };
 
 struct ListTcArgs {
@@ -501,7 +501,8 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
         __syncwarp();
     } else if (ROWS && warp >= 6 + kEpi) {
         // ------------------------------------------------- rows of dK to memory
-        const int quarter = warp & 3, lrow = quarter * 32 + lane;
+        // two groups of four on alternate tiles
+        const int quarter = warp & 3, lrow = quarter * 32 + lane, grp = (warp - 6 - kEpi) >> 2;
         int n = 0;
         bool alive = true;
         RowDesc nx = t0 < n_q ? a.l.rows[t0] : none;
@@ -523,23 +524,23 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
                 return __ldg(a.base + s / kPosBlock) + __ldg(a.off + s) + __ldg(a.pre + word + s) +
                        __popc(__ldg(a.bits + word + s) & below);
             };
-            uint32_t at = nt > 0 ? place(key_row(0)) : 0u;
-            int s_next = nt > 1 ? key_row(1) : 0;
-            for (int i = 0; i < nt && alive; ++i, ++n) {
-                const int b = n & 1;
+            const int i0 = (n & 1) == grp ? 0 : 1;   // the group's first tile
+            uint32_t at = i0 < nt ? place(key_row(i0)) : 0u;
+            int s_next = i0 + 2 < nt ? key_row(i0 + 2) : 0;
+            for (int i = i0; i < nt && alive; i += 2) {
                 const uint32_t mine = at;
-                if (i + 1 < nt) at = place(s_next);
-                if (i + 2 < nt) s_next = key_row(i + 2);
-                alive = tc_wait_warp(&dkfull[b], (n >> 1) & 1, status, 36, abort_flag, alive);
+                if (i + 2 < nt) at = place(s_next);
+                if (i + 4 < nt) s_next = key_row(i + 4);
+                alive = tc_wait_warp(&dkfull[grp], ((n + i) >> 1) & 1, status, 36, abort_flag, alive);
                 if (!alive) break;
                 tc_fence_after();
                 // Through shared memory, so that eight lanes store a whole 128-byte line: a lane storing its
                 // own row took four times the requests (1.58 ms for 4096 queries of 2048 places).
-                float4* tile = reinterpret_cast<float4*>(smem + SH::x_off(n_stages)) + quarter * 256;
+                float4* tile = reinterpret_cast<float4*>(smem + SH::x_off(n_stages)) + (grp * 4 + quarter) * 256;
 #pragma unroll
                 for (int c = 0; c < D; c += 32) {
                     float v[32];
-                    tmem_load<32>(tmem + 256 + b * 128 + c + ((uint32_t)(quarter * 32) << 16), v);
+                    tmem_load<32>(tmem + 256 + grp * 128 + c + ((uint32_t)(quarter * 32) << 16), v);
 #pragma unroll
                     for (int x = 0; x < 8; ++x)
                         tile[lane * 8 + (x ^ (lane & 7))] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
@@ -555,8 +556,9 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
                     __syncwarp();
                 }
                 tc_fence_before();
-                mbar_arrive(&dkfree[b]);
+                mbar_arrive(&dkfree[grp]);
             }
+            n += nt;
         }
     } else {
         // ---------------------------------------------------------- epilogue
