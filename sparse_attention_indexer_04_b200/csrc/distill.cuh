@@ -17,6 +17,8 @@
 
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace dsa {
@@ -48,20 +50,28 @@ __device__ __forceinline__ void distill_load(const X* p, int c, int k, V* v)
 {
     if (VEC == 4 && (!EDGE || (c >= 0 && c + 3 < k))) {
         if constexpr (sizeof(X) == 2) {
-            const uint2 a = __ldcs(reinterpret_cast<const uint2*>(p + c));
+            const uint2 a = *reinterpret_cast<const uint2*>(p + c);
             v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xffff0000u);
             v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xffff0000u);
         } else if constexpr (sizeof(V) == sizeof(int32_t) && V(0.5f) == V(0)) {
-            const int4 a = __ldcs(reinterpret_cast<const int4*>(p + c));
+            const int4 a = *reinterpret_cast<const int4*>(p + c);
             v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
         } else {
-            const float4 a = __ldcs(reinterpret_cast<const float4*>(p + c));
+            const float4 a = *reinterpret_cast<const float4*>(p + c);
             v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
         }
     } else {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) v[e] = !EDGE || (c + e >= 0 && c + e < k) ? (V)p[c + e] : V(0);
     }
+}
+
+template <int BYTES>
+__device__ __forceinline__ void distill_copy(void* dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "n"(BYTES)
+                 : "memory");
 }
 
 // Joint reductions over the T threads of a row: a warp's lanes (T = 32) or the whole CTA.
@@ -228,6 +238,110 @@ __global__ void __launch_bounds__(NT) distill_kernel(const __grid_constant__ Dis
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
                 if (!EDGE || (c + e >= 0 && c + e < a.k)) dp[c + e] = v[e];
+        }
+    }
+}
+
+// One row at a time per CTA, rows NT * 4 * (NV - 1) < k <= NT * 4 * NV long, with the next row's places on
+// their way to shared memory while this one is worked on (a CTA per row holds so many registers that
+// it is alone on its SM, and its loads, sums and stores then follow one another: 78 us for
+// 1021 x 20011).  A thread copies the places that it reads itself, so it waits for its own copies alone;
+// vectors that hang over a row's ends are loaded when they are needed.
+template <typename TT, bool EDGE, int NV, int NT>
+__global__ void __launch_bounds__(NT, 1) distill_ring_kernel(const __grid_constant__ DistillArgs a)
+{
+    extern __shared__ __align__(16) uint8_t dyn[];
+    __shared__ float4 red1[32], red2[32];
+    const int t = threadIdx.x;
+    float4* ss = reinterpret_cast<float4*>(dyn);                                    // [NV][NT] scores
+    int4* sl = reinterpret_cast<int4*>(ss + NV * NT);                               // [NV][NT] lists, if given
+    using Quad = typename std::conditional<sizeof(TT) == 2, uint2, float4>::type;
+    Quad* st = reinterpret_cast<Quad*>(a.list ? sl + NV * NT : sl);                 // [NV][NT] teacher
+    auto start = [&](int64_t row) { return EDGE ? -int((a.off0 + row * a.off_step) & 3) : 0; };
+    auto whole = [&](int c) { return !EDGE || (c >= 0 && c + 3 < a.k); };
+    auto fetch = [&](int64_t row) {
+        if (row < a.n) {
+            const int c0 = start(row);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = c0 + (i * NT + t) * 4;
+                if (c >= a.k || !whole(c)) continue;
+                distill_copy<16>(ss + i * NT + t, a.s + row * a.ld_s + c);
+                distill_copy<sizeof(Quad)>(st + i * NT + t, static_cast<const TT*>(a.t) + row * a.ld_t + c);
+                if (a.list) distill_copy<16>(sl + i * NT + t, a.list + row * a.ld_list + c);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch(blockIdx.x);
+    for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        const int c0 = start(row);
+        float s[NV][4], f[NV][4];
+        float ms = -CUDART_INF_F, mt = -CUDART_INF_F;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = c0 + (i * NT + t) * 4;
+            int32_t l[4] = {0, 0, 0, 0};
+            if (c >= a.k) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) { s[i][e] = -CUDART_INF_F; f[i][e] = 0.f; }
+            } else if (whole(c)) {
+                distill_load<4, false>(reinterpret_cast<const float*>(ss + i * NT + t), 0, 4, s[i]);
+                distill_load<4, false>(reinterpret_cast<const TT*>(st + i * NT + t), 0, 4, f[i]);
+                if (a.list) distill_load<4, false>(reinterpret_cast<const int32_t*>(sl + i * NT + t), 0, 4, l);
+            } else {
+                distill_load<4, true>(a.s + row * a.ld_s, c, a.k, s[i]);
+                distill_load<4, true>(static_cast<const TT*>(a.t) + row * a.ld_t, c, a.k, f[i]);
+                if (a.list) distill_load<4, true>(a.list + row * a.ld_list, c, a.k, l);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < 0 || c + e >= a.k) s[i][e] = -CUDART_INF_F;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (l[e] < 0) s[i][e] = -CUDART_INF_F;
+                if (s[i][e] == -CUDART_INF_F) f[i][e] = a.weights ? 0.f : -CUDART_INF_F;
+                ms = fmaxf(ms, s[i][e]);
+                mt = fmaxf(mt, f[i][e]);
+            }
+        }
+        distill_max2<NT>(ms, mt, red1);
+        fetch(row + gridDim.x);   // behind the barrier: every value has left shared memory
+        float z = 0.f, y = 0.f, x = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool in = s[i][e] != -CUDART_INF_F;
+                const float d = (s[i][e] - ms) * a.scale;
+                s[i][e] = in ? distill_exp2(d) : 0.f;
+                z += s[i][e];
+                float c = 0.f, w = 0.f;
+                if (in && mt != -CUDART_INF_F) w = distill_weight(f[i][e], mt, a, c);
+                f[i][e] = w;
+                y += w;
+                if (w != 0.f) x = fmaf(w, c - d, x);
+            }
+        distill_sum3<NT>(z, y, x, red2);
+        const DistillRow r = distill_row(z, y, x, a.g ? a.g[row] : 1.f, a);
+        if (t == 0 && a.loss) a.loss[row] = r.loss;
+        if (!a.ds) continue;
+        float* dp = a.ds + row * a.ld_ds;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = c0 + (i * NT + t) * 4;
+            if (c >= a.k) continue;
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = s[i][e] == 0.f && f[i][e] == 0.f ? 0.f : s[i][e] * r.cs - f[i][e] * r.ct;
+            if (whole(c)) {
+                *reinterpret_cast<float4*>(dp + c) = make_float4(v[0], v[1], v[2], v[3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e >= 0 && c + e < a.k) dp[c + e] = v[e];
+            }
         }
     }
 }

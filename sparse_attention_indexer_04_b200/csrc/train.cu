@@ -133,6 +133,17 @@ dsa_status distill_launch(const DistillArgs& a, cudaStream_t st)
     return launched();
 }
 
+template <typename TT, bool EDGE, int NV, int NT>
+dsa_status distill_ring(const DistillArgs& a, cudaStream_t st)
+{
+    const auto kern = distill_ring_kernel<TT, EDGE, NV, NT>;
+    const size_t smem = size_t(NV) * NT * (16 + 4 * sizeof(TT) + (a.list ? 16 : 0));
+    dsa_status s = set_smem(kern, smem);
+    if (s != DSA_OK) return s;
+    DSA_LAUNCH(kProfDistill, st, kern<<<std::min(a.n, 148), NT, smem, st>>>(a));
+    return launched();
+}
+
 template <typename TT, int VEC, bool EDGE>
 dsa_status distill_pick(const DistillArgs& a, cudaStream_t st)
 {
@@ -145,6 +156,11 @@ dsa_status distill_pick(const DistillArgs& a, cudaStream_t st)
     if (k <= 2048) return distill_launch<TT, VEC, EDGE, 128, 4 * U, 128>(a, st);
     if (k <= 4096) return distill_launch<TT, VEC, EDGE, 256, 4 * U, 256>(a, st);
     if (k <= 8192) return distill_launch<TT, VEC, EDGE, 512, 4 * U, 512>(a, st);
+    if constexpr (VEC == 4) {   // longer rows, as many as shared memory holds, read ahead
+        if (k <= 12288) return distill_ring<TT, EDGE, 6, 512>(a, st);
+        if (k <= 16384 && !a.list) return distill_ring<TT, EDGE, 8, 512>(a, st);
+        if (k <= 20480 && !a.list) return distill_ring<TT, EDGE, 10, 512>(a, st);
+    }
     if (k <= 16384) return distill_launch<TT, VEC, EDGE, 1024, 4 * U, 1024>(a, st);
     if (k <= kDistillRegCols) return distill_launch<TT, VEC, EDGE, 1024, 5 * U, 1024>(a, st);
     DSA_LAUNCH(kProfDistill, st, distill_long_kernel<TT, 512><<<a.n, 512, 0, st>>>(a));
