@@ -247,8 +247,8 @@ __global__ void __launch_bounds__(NT) distill_kernel(const __grid_constant__ Dis
 // it is alone on its SM, and its loads, sums and stores then follow one another: 78 us for
 // 1021 x 20011).  A thread copies the places that it reads itself, so it waits for its own copies alone;
 // vectors that hang over a row's ends are loaded when they are needed.
-template <typename TT, bool EDGE, int NV, int NT>
-__global__ void __launch_bounds__(NT, 1) distill_ring_kernel(const __grid_constant__ DistillArgs a)
+template <typename TT, bool EDGE, int NV, int NT, int CTAS>
+__global__ void __launch_bounds__(NT, CTAS) distill_ring_kernel(const __grid_constant__ DistillArgs a)
 {
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ float4 red1[32], red2[32];
