@@ -196,8 +196,12 @@ struct ListPlan {
     float* acc;         // by_rows, more than one launch: sums so far
 };
 
-// Bytes of dK rows kept between two launches: 888 queries of 2048 places at d = 128, six a CTA.
+// Bytes of dK rows kept between two launches (888 queries of 2048 places at d = 128, six a CTA), and of
+// the bits and counts that place them (6 bytes per key and 32 queries).
 constexpr size_t kRowsBudget = size_t(1024) << 20;
+constexpr int32_t kRowsMaxQueries = 32768;   // (counts of 16 bits)
+// Bytes of partial dK of the dense form at most.
+constexpr size_t kPartsBudget = size_t(4096) << 20;
 
 // What a batch's lists hold, as far as the host knows: the queries of a sequence taken as its last ones
 // (a training batch: all of them; a chunk at the end of a context).
@@ -266,14 +270,16 @@ size_t list_plan(char* base, const dsa_batch* b, const HostInfo& hi, int32_t k, 
     }
     p->rows = c.take<RowDesc>(std::max(1, b->num_queries));
     if (!backward) return c.off;
-    p->by_rows = dk_by_rows(b, k);
     p->key_blocks = (hi.max_k + kDkKeys - 1) / kDkKeys;
     p->units = b->num_keys / kDkKeys + b->num_seqs;
     p->parts = dk_parts(p->units, hi.max_q);
+    p->by_rows = dk_by_rows(b, k) || (p->parts > 1 && size_t(p->parts) * b->num_keys * b->head_dim * 4 > kPartsBudget);
     if (p->by_rows) {
         const int64_t row = std::min(k, std::max(1, hi.max_k));   // places of a query at most
         const int64_t fit = int64_t(kRowsBudget / (size_t(row) * b->head_dim * 4));
-        p->chunk = (int32_t)std::min<int64_t>(b->num_queries, fit > 148 ? fit / 148 * 148 : std::max<int64_t>(1, fit));
+        const int64_t words = std::max<int64_t>(1, int64_t(kRowsBudget / (6 * size_t(std::max(1, b->num_keys)))));
+        const int64_t most = std::min({fit, 32 * words, int64_t(kRowsMaxQueries)});
+        p->chunk = (int32_t)std::min<int64_t>(b->num_queries, most > 148 ? most / 148 * 148 : std::max<int64_t>(1, most));
         p->words = (p->chunk + 31) / 32;
         p->part = c.take<float>(size_t(p->chunk) * row * b->head_dim);
         p->bits = c.take<uint32_t>(size_t(p->words) * b->num_keys);

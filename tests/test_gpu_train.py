@@ -560,3 +560,23 @@ def test_binding_refuses_what_the_library_cannot_read():
                 lambda: dsa.list_scores_backward(lay, Q, K, W, idx, idx)):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_many_queries_of_short_lists():
+    """More queries than one launch of the rows takes (16-bit counts: 32,768), every one listing the same key: the
+    key's gradient is the sum over all of them, and the sums carry over."""
+    n = 33000
+    g = gen(97)
+    b = workloads.ragged(97, [n], [600], H=4, d=32, k=1, integer=True)
+    b.q_pos[:] = 599
+    lists = torch.full((n, 1), 5, dtype=torch.int32)
+    ds = torch.randint(-1, 2, (n, 1), generator=g).float()
+    lay, Q, K, W = on_gpu(b)
+    dQ, dK, dW = dsa.list_scores_backward(lay, Q, K, W, lists.to(DEV), ds.to(DEV))
+    S = torch.einsum("thd,d->th", b.Q.double(), b.K[5].double())
+    G = torch.where(S > 0, ds.double() * b.W.double(), 0.0)
+    want = torch.zeros(600, 32).double()
+    want[5] = torch.einsum("th,thd->d", G, b.Q.double())          # integers and quarters: exact in fp32
+    assert torch.equal(dK.cpu(), want.bfloat16())
+    assert torch.equal(dQ.cpu(), (G[:, :, None] * b.K[5].double()).bfloat16())
+    assert torch.equal(dW.cpu(), (ds.double() * S.clamp(min=0)).float())
