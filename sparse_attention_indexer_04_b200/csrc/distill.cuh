@@ -37,7 +37,6 @@ struct DistillArgs {
     float* ds;             // NULL: not written
     int64_t ld_ds;
     int32_t n, k;
-    int32_t weights;       // the teacher's values: 0 logits, 1 weights
     float inv_tau;
     float scale;           // log2(e) / tau: exponents are taken to base 2
     int32_t off0, off_step; // VEC 4: row r starts (off0 + r * off_step) % 4 places behind a 4-place boundary
@@ -139,34 +138,75 @@ __device__ __forceinline__ float distill_log2(float x)
     return y;
 }
 
-// The teacher's unnormalised weight of a counted place and its base-2 logarithm c.
+// The teacher's unnormalised weight of a place and its base-2 logarithm c (a logit of -inf: 0 and -inf).
+template <bool WEIGHTS>
 __device__ __forceinline__ float distill_weight(float t, float mt, const DistillArgs& a, float& c)
 {
-    if (a.weights) {
+    if constexpr (WEIGHTS) {
         c = distill_log2(t);
         return t;
+    } else {
+        c = (t - mt) * a.scale;
+        return distill_exp2(c);
     }
-    c = (t - mt) * a.scale;
-    return distill_exp2(c);
+}
+
+// N places in registers: s scores (-inf where a place does not count), f the teacher's values (then 0 or
+// -inf).  Raises the row's maxima.
+template <bool WEIGHTS, int N>
+__device__ __forceinline__ void distill_maxima(const float* s, float* f, float& ms, float& mt)
+{
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        if (s[e] == -CUDART_INF_F) f[e] = WEIGHTS ? 0.f : -CUDART_INF_F;
+        ms = fmaxf(ms, s[e]);
+        if (!WEIGHTS) mt = fmaxf(mt, f[e]);
+    }
+}
+
+// From the row's maxima (0 in place of -inf, so that -inf gives weight 0): s becomes e^a, f the teacher's
+// weight; their sums and the cross sum grow.
+template <bool WEIGHTS, int N>
+__device__ __forceinline__ void distill_sums(float* s, float* f, float ms, float mt, const DistillArgs& a, float& z,
+                                             float& y, float& x)
+{
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const float d = (s[e] - ms) * a.scale;
+        s[e] = distill_exp2(d);
+        z += s[e];
+        float c;
+        f[e] = distill_weight<WEIGHTS>(f[e], mt, a, c);
+        y += f[e];
+        if (f[e] != 0.f) x = fmaf(f[e], c - d, x);
+    }
 }
 
 // What a row's sums say: the loss, and the factors of e^a and f in the gradient.
 struct DistillRow {
     float loss, cs, ct;
+    bool sound;   // the factors are finite
 };
 
 __device__ __forceinline__ DistillRow distill_row(float z, float y, float x, float g, const DistillArgs& a)
 {
-    DistillRow r{0.f, 0.f, 0.f};
+    DistillRow r{0.f, 0.f, 0.f, true};
     if (y == 0.f || z == 0.f) return r;   // no counted place, or none that the teacher weighs: nothing to learn
     r.loss = x / y * 0.69314718055994531f + (logf(z) - logf(y));
     r.cs = g * a.inv_tau / z;
     r.ct = g * a.inv_tau / y;
+    r.sound = isfinite(r.cs) && isfinite(r.ct);
     return r;
 }
 
+// A place's gradient: 0 where neither has weight, whatever a NaN elsewhere in the row made of the factors.
+__device__ __forceinline__ float distill_grad(float s, float f, const DistillRow& r)
+{
+    return r.sound ? s * r.cs - f * r.ct : s == 0.f && f == 0.f ? 0.f : s * r.cs - f * r.ct;
+}
+
 // One row per group of T threads (T = 32: NT / 32 rows per CTA; else T == NT), in registers.
-template <typename TT, int VEC, bool EDGE, int T, int NV, int NT>
+template <typename TT, bool WEIGHTS, int VEC, bool EDGE, int T, int NV, int NT>
 __global__ void __launch_bounds__(NT) distill_kernel(const __grid_constant__ DistillArgs a)
 {
     __shared__ float4 red1[32], red2[32];
@@ -196,29 +236,13 @@ __global__ void __launch_bounds__(NT) distill_kernel(const __grid_constant__ Dis
     }
     float ms = -CUDART_INF_F, mt = -CUDART_INF_F;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            if (s[i][e] == -CUDART_INF_F) f[i][e] = a.weights ? 0.f : -CUDART_INF_F;   // not counted: no value either
-            ms = fmaxf(ms, s[i][e]);
-            mt = fmaxf(mt, f[i][e]);
-        }
+    for (int i = 0; i < NV; ++i) distill_maxima<WEIGHTS, VEC>(s[i], f[i], ms, mt);
     distill_max2<T>(ms, mt, red1);
+    ms = ms == -CUDART_INF_F ? 0.f : ms;
+    mt = mt == -CUDART_INF_F ? 0.f : mt;
     float z = 0.f, y = 0.f, x = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const bool in = s[i][e] != -CUDART_INF_F;
-            const float d = (s[i][e] - ms) * a.scale;
-            s[i][e] = in ? distill_exp2(d) : 0.f;
-            z += s[i][e];
-            float c = 0.f, w = 0.f;
-            if (in && mt != -CUDART_INF_F) w = distill_weight(f[i][e], mt, a, c);
-            f[i][e] = w;
-            y += w;
-            if (w != 0.f) x = fmaf(w, c - d, x);
-        }
+    for (int i = 0; i < NV; ++i) distill_sums<WEIGHTS, VEC>(s[i], f[i], ms, mt, a, z, y, x);
     distill_sum3<T>(z, y, x, red2);
     const DistillRow r = distill_row(z, y, x, a.g ? a.g[row] : 1.f, a);
     if (t == 0 && a.loss) a.loss[row] = r.loss;
@@ -230,8 +254,7 @@ __global__ void __launch_bounds__(NT) distill_kernel(const __grid_constant__ Dis
         if (c >= a.k) continue;
         float v[VEC];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)   // 0 where neither has weight, whatever a NaN elsewhere made of the factors
-            v[e] = s[i][e] == 0.f && f[i][e] == 0.f ? 0.f : s[i][e] * r.cs - f[i][e] * r.ct;
+        for (int e = 0; e < VEC; ++e) v[e] = distill_grad(s[i][e], f[i][e], r);
         if (VEC == 4 && (!EDGE || (c >= 0 && c + 3 < a.k))) {
             *reinterpret_cast<float4*>(dp + c) = make_float4(v[0], v[VEC / 4], v[VEC / 2], v[VEC - 1]);
         } else {
@@ -247,7 +270,7 @@ __global__ void __launch_bounds__(NT) distill_kernel(const __grid_constant__ Dis
 // it is alone on its SM, and its loads, sums and stores then follow one another: 78 us for
 // 1021 x 20011).  A thread copies the places that it reads itself, so it waits for its own copies alone;
 // vectors that hang over a row's ends are loaded when they are needed.
-template <typename TT, bool EDGE, int NV, int NT, int CTAS>
+template <typename TT, bool WEIGHTS, bool EDGE, int NV, int NT, int CTAS>
 __global__ void __launch_bounds__(NT, CTAS) distill_ring_kernel(const __grid_constant__ DistillArgs a)
 {
     extern __shared__ __align__(16) uint8_t dyn[];
@@ -299,30 +322,17 @@ __global__ void __launch_bounds__(NT, CTAS) distill_ring_kernel(const __grid_con
                     if (c + e < 0 || c + e >= a.k) s[i][e] = -CUDART_INF_F;
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 4; ++e)
                 if (l[e] < 0) s[i][e] = -CUDART_INF_F;
-                if (s[i][e] == -CUDART_INF_F) f[i][e] = a.weights ? 0.f : -CUDART_INF_F;
-                ms = fmaxf(ms, s[i][e]);
-                mt = fmaxf(mt, f[i][e]);
-            }
+            distill_maxima<WEIGHTS, 4>(s[i], f[i], ms, mt);
         }
         distill_max2<NT>(ms, mt, red1);
         fetch(row + gridDim.x);   // behind the barrier: every value has left shared memory
+        ms = ms == -CUDART_INF_F ? 0.f : ms;
+        mt = mt == -CUDART_INF_F ? 0.f : mt;
         float z = 0.f, y = 0.f, x = 0.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const bool in = s[i][e] != -CUDART_INF_F;
-                const float d = (s[i][e] - ms) * a.scale;
-                s[i][e] = in ? distill_exp2(d) : 0.f;
-                z += s[i][e];
-                float c = 0.f, w = 0.f;
-                if (in && mt != -CUDART_INF_F) w = distill_weight(f[i][e], mt, a, c);
-                f[i][e] = w;
-                y += w;
-                if (w != 0.f) x = fmaf(w, c - d, x);
-            }
+        for (int i = 0; i < NV; ++i) distill_sums<WEIGHTS, 4>(s[i], f[i], ms, mt, a, z, y, x);
         distill_sum3<NT>(z, y, x, red2);
         const DistillRow r = distill_row(z, y, x, a.g ? a.g[row] : 1.f, a);
         if (t == 0 && a.loss) a.loss[row] = r.loss;
@@ -334,7 +344,7 @@ __global__ void __launch_bounds__(NT, CTAS) distill_ring_kernel(const __grid_con
             if (c >= a.k) continue;
             float v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = s[i][e] == 0.f && f[i][e] == 0.f ? 0.f : s[i][e] * r.cs - f[i][e] * r.ct;
+            for (int e = 0; e < 4; ++e) v[e] = distill_grad(s[i][e], f[i][e], r);
             if (whole(c)) {
                 *reinterpret_cast<float4*>(dp + c) = make_float4(v[0], v[1], v[2], v[3]);
             } else {
@@ -349,7 +359,7 @@ __global__ void __launch_bounds__(NT, CTAS) distill_ring_kernel(const __grid_con
 // Rows of any length: one CTA per row, two sweeps.  In the first a thread keeps running maxima and
 // sums, rescaled when a batch of places raises a maximum; the CTA then brings its threads' sums to the
 // row's maxima and joins them; the second writes the gradient.
-template <typename TT, int NT>
+template <typename TT, bool WEIGHTS, int NT>
 __global__ void __launch_bounds__(NT) distill_long_kernel(const __grid_constant__ DistillArgs a)
 {
     __shared__ float4 red1[32], red2[32];
@@ -369,7 +379,7 @@ __global__ void __launch_bounds__(NT) distill_long_kernel(const __grid_constant_
         }
 #pragma unroll
         for (int i = 0; i < BATCH; ++i)
-            if (s[i] == -CUDART_INF_F) v[i] = a.weights ? 0.f : -CUDART_INF_F;
+            if (s[i] == -CUDART_INF_F) v[i] = WEIGHTS ? 0.f : -CUDART_INF_F;
     };
     // to maxima m and n: exponents shift by (m - ms) and, for logits, (n - mt); with nothing summed yet the
     // old maximum is -inf and the sums are zero whatever they are scaled by
@@ -381,7 +391,7 @@ __global__ void __launch_bounds__(NT) distill_long_kernel(const __grid_constant_
             x = fmaf(y, up, x);
             ms = m;
         }
-        if (!a.weights && n > mt) {
+        if (!WEIGHTS && n > mt) {
             const float up = mt == -CUDART_INF_F ? 0.f : (n - mt) * a.scale, f = distill_exp2(-up);
             x = (x - y * up) * f;
             y *= f;
@@ -403,7 +413,7 @@ __global__ void __launch_bounds__(NT) distill_long_kernel(const __grid_constant_
             const float d = (s[i] - ms) * a.scale;
             z += distill_exp2(d);
             float lg, w = 0.f;
-            if (a.weights || mt != -CUDART_INF_F) w = distill_weight(v[i], mt, a, lg);
+            if (WEIGHTS || mt != -CUDART_INF_F) w = distill_weight<WEIGHTS>(v[i], mt, a, lg);
             y += w;
             if (w != 0.f) x = fmaf(w, lg - d, x);
         }
@@ -425,7 +435,7 @@ __global__ void __launch_bounds__(NT) distill_long_kernel(const __grid_constant_
             float lg, out = 0.f;
             if (s[i] != -CUDART_INF_F) {
                 out = distill_exp2((s[i] - ms) * a.scale) * r.cs;
-                if (a.weights || mt != -CUDART_INF_F) out -= distill_weight(v[i], mt, a, lg) * r.ct;
+                if (WEIGHTS || mt != -CUDART_INF_F) out -= distill_weight<WEIGHTS>(v[i], mt, a, lg) * r.ct;
             }
             dp[c] = out;
         }

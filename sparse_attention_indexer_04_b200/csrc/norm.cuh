@@ -12,7 +12,7 @@
 // partial row, and a second kernel adds the partial rows column by column.
 #pragma once
 
-#include "common.cuh"
+#include "ptx.cuh"
 
 namespace dsa {
 
@@ -39,6 +39,7 @@ struct NormArgs {
 template <typename TX, int VEC>
 struct NormRaw {
     TX v;
+    __device__ __forceinline__ void zero() { v = TX(0.f); }
     __device__ __forceinline__ void load(const TX* p) { v = *p; }
     __device__ __forceinline__ void get(float* f) const { f[0] = (float)v; }
 };
@@ -46,6 +47,7 @@ struct NormRaw {
 template <>
 struct NormRaw<float, 8> {
     float4 a, b;
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ void load(const float* p)
     {
         a = *reinterpret_cast<const float4*>(p);
@@ -61,6 +63,7 @@ struct NormRaw<float, 8> {
 template <>
 struct NormRaw<__nv_bfloat16, 8> {
     uint4 a;
+    __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void get(float* f) const
     {
@@ -108,6 +111,109 @@ __device__ __forceinline__ void norm_store_vec(__nv_bfloat16* p, const float* v)
     }
 }
 
+// Arithmetic on N values in registers, two to an instruction where N is even: with one value an
+// instruction, 16-bit rows were bound by the issue of instructions (two thirds of the slots), not by
+// memory.  Every element is rounded as in the plain form.
+__device__ __forceinline__ uint64_t norm_add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t norm_mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// v += s
+template <int N>
+__device__ __forceinline__ void norm_shift(float* v, float s)
+{
+    if constexpr (N % 2 == 0) {
+        const uint64_t ss = pack_f32x2(s, s);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) unpack_f32x2(norm_add2(pack_f32x2(v[i], v[i + 1]), ss), v[i], v[i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += s;
+    }
+}
+
+// v *= s
+template <int N>
+__device__ __forceinline__ void norm_scale(float* v, float s)
+{
+    if constexpr (N % 2 == 0) {
+        const uint64_t ss = pack_f32x2(s, s);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) unpack_f32x2(norm_mul2(pack_f32x2(v[i], v[i + 1]), ss), v[i], v[i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] *= s;
+    }
+}
+
+// v *= w
+template <int N>
+__device__ __forceinline__ void norm_times(float* v, const float* w)
+{
+    if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+            unpack_f32x2(norm_mul2(pack_f32x2(v[i], v[i + 1]), pack_f32x2(w[i], w[i + 1])), v[i], v[i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] *= w[i];
+    }
+}
+
+// acc += v
+template <int N>
+__device__ __forceinline__ void norm_add(float* acc, const float* v)
+{
+    if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+            unpack_f32x2(norm_add2(pack_f32x2(acc[i], acc[i + 1]), pack_f32x2(v[i], v[i + 1])), acc[i], acc[i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] += v[i];
+    }
+}
+
+// acc = a * b + acc
+template <int N>
+__device__ __forceinline__ void norm_fma(float* acc, const float* a, const float* b)
+{
+    if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+            unpack_f32x2(fma_f32x2(pack_f32x2(a[i], a[i + 1]), pack_f32x2(b[i], b[i + 1]), pack_f32x2(acc[i], acc[i + 1])),
+                         acc[i], acc[i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = fmaf(a[i], b[i], acc[i]);
+    }
+}
+
+// acc = a * s + acc
+template <int N>
+__device__ __forceinline__ void norm_fma(float* acc, const float* a, float s)
+{
+    if constexpr (N % 2 == 0) {
+        const uint64_t ss = pack_f32x2(s, s);
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+            unpack_f32x2(fma_f32x2(pack_f32x2(a[i], a[i + 1]), ss, pack_f32x2(acc[i], acc[i + 1])), acc[i], acc[i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = fmaf(a[i], s, acc[i]);
+    }
+}
+
 // Sum of (a, b) over the T threads of a row group: lanes of one warp, or the whole CTA (T == NT).
 // `red` (32 entries) must not be in use by a sum that some thread may still be reading: callers
 // alternate between two.
@@ -151,40 +257,38 @@ __global__ void __launch_bounds__(NT) layer_norm_kernel(const __grid_constant__ 
         for (int i = 0; i < NV; ++i) {
             const int64_t row = row0 + k * G;
             const int c = (i * T + t) * VEC;
+            raw[k][i].zero();   // (what lies outside the row counts for nothing)
             if (row < a.n && c < a.d) raw[k][i].load(static_cast<const TX*>(a.x) + row * a.ld_x + c);
         }
+    constexpr int S = VEC == 8 ? 2 : 1;   // running sums of a thread
 #pragma unroll
     for (int k = 0; k < R; ++k) {
         const int64_t row = row0 + k * G;
-        const bool live = row < a.n;
         float v[NV][VEC];
-        float s = 0.f, unused = 0.f;
+        float s[S], q[S], unused = 0.f;
+#pragma unroll
+        for (int e = 0; e < S; ++e) s[e] = q[e] = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const bool in = live && (i * T + t) * VEC < a.d;
             raw[k][i].get(v[i]);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                v[i][e] = in ? v[i][e] : 0.f;
-                s += v[i][e];
-            }
+            for (int e = 0; e < VEC; e += S) norm_add<S>(s, v[i] + e);
         }
-        norm_group_sum<T>(s, unused, red[0]);
-        const float mu = s * inv_d;
-        float q = 0.f;
+        float sum = S == 2 ? s[0] + s[S - 1] : s[0];
+        norm_group_sum<T>(sum, unused, red[0]);
+        const float mu = sum * inv_d;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const bool in = (i * T + t) * VEC < a.d;
+            norm_shift<VEC>(v[i], -mu);
+            if ((i * T + t) * VEC < a.d)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                v[i][e] -= mu;
-                q = in ? fmaf(v[i][e], v[i][e], q) : q;
-            }
+                for (int e = 0; e < VEC; e += S) norm_fma<S>(q, v[i] + e, v[i] + e);
         }
+        sum = S == 2 ? q[0] + q[S - 1] : q[0];
         unused = 0.f;
-        norm_group_sum<T>(q, unused, red[1]);
-        const float r = 1.f / sqrtf(fmaf(q, inv_d, a.eps));
-        if (!live) continue;
+        norm_group_sum<T>(sum, unused, red[1]);
+        const float r = 1.f / sqrtf(fmaf(sum, inv_d, a.eps));
+        if (row >= a.n) continue;
         if (t == 0) {
             if (a.mean) a.mean[row] = mu;
             if (a.rstd) a.rstd[row] = r;
@@ -199,17 +303,23 @@ __global__ void __launch_bounds__(NT) layer_norm_kernel(const __grid_constant__ 
             for (int e = 0; e < VEC; ++e) { w[e] = 1.f; b[e] = 0.f; }
             if (a.w) norm_load_vec<VEC>(a.w + c, w);
             if (a.b) norm_load_vec<VEC>(a.b + c, b);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) v[i][e] = fmaf(v[i][e] * r, w[e], b[e]);
-            norm_store_vec<VEC>(y + c, v[i]);
+            norm_scale<VEC>(v[i], r);
+            norm_fma<VEC>(b, v[i], w);
+            norm_store_vec<VEC>(y + c, b);
         }
     }
 }
 
+// CTAs of the backward kernel an SM holds: 768 threads of up to 80 registers (1024 of 64 spill, and CTAs
+// past the resident ones ran as a second wave: 131072 x 128 fp32 45 us against 38), or one of 1024
+// (whose launch bounds name no count: given 1, the compiler moved the loads behind the sums, 74 us
+// against 56 for 4099 x 5001).
+constexpr int norm_bwd_per_sm(int threads) { return threads >= 1024 ? 1 : 768 / threads; }
+
 // TX: the type of x and dx, TY: of dy.  A group walks its rows with the next one's loads in flight
 // behind the current one's sums: without that, a group waits out the memory's latency once a row.
 template <typename TX, typename TY, int VEC, int T, int NV, int NT>
-__global__ void __launch_bounds__(NT) layer_norm_bwd_kernel(const __grid_constant__ NormArgs a)
+__global__ void __launch_bounds__(NT, NT < 1024 ? norm_bwd_per_sm(NT) : 0) layer_norm_bwd_kernel(const __grid_constant__ NormArgs a)
 {
     __shared__ float2 red[2][32];
     constexpr int G = NT / T;
@@ -224,6 +334,13 @@ __global__ void __launch_bounds__(NT) layer_norm_bwd_kernel(const __grid_constan
     NormRaw<TY, VEC> ry[NV];
     float mu_next = 0.f, r_next = 0.f;
     auto read = [&](int64_t row) {
+        if constexpr (VEC == 8) {   // places outside the rows are zeros in dy, which keeps them out of every sum
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                rx[i].zero();
+                ry[i].zero();
+            }
+        }
         if (row >= a.n) return;
         const TX* x = static_cast<const TX*>(a.x) + row * a.ld_x;
         const TY* dy = static_cast<const TY*>(a.dy) + row * a.ld_dy;
@@ -252,26 +369,42 @@ __global__ void __launch_bounds__(NT) layer_norm_bwd_kernel(const __grid_constan
         }
         const float mu = mu_next, r = r_next;
         read(row + step);
-        float s1 = 0.f, s2 = 0.f;   // sums of g and of g xh
+        constexpr int S = VEC == 8 ? 2 : 1;
+        float a1[S], a2[S];   // sums of g and of g xh
+#pragma unroll
+        for (int e = 0; e < S; ++e) a1[e] = a2[e] = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * T + t) * VEC;
-            const bool in = live && c < a.d;
-            float w[VEC];
+            if constexpr (VEC == 8) {
+                norm_shift<VEC>(xh[i], -mu);
+                norm_scale<VEC>(xh[i], r);
+                norm_fma<VEC>(dw[i], gy[i], xh[i]);
+                norm_add<VEC>(db[i], gy[i]);
+                if (a.w && c < a.d) {
+                    float w[VEC];
+                    norm_load_vec<VEC>(a.w + c, w);   // from L1 after the first row
+                    norm_times<VEC>(gy[i], w);
+                }
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) w[e] = 1.f;
-            if (a.w && c < a.d) norm_load_vec<VEC>(a.w + c, w);   // from L1 after the first row
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                xh[i][e] = in ? (xh[i][e] - mu) * r : 0.f;
-                gy[i][e] = in ? gy[i][e] : 0.f;
-                dw[i][e] = fmaf(gy[i][e], xh[i][e], dw[i][e]);
-                db[i][e] += gy[i][e];
-                gy[i][e] *= w[e];
-                s1 += gy[i][e];
-                s2 = fmaf(gy[i][e], xh[i][e], s2);
+                for (int e = 0; e < VEC; e += S) {
+                    norm_add<S>(a1, gy[i] + e);
+                    norm_fma<S>(a2, gy[i] + e, xh[i] + e);
+                }
+            } else {
+                const bool in = live && c < a.d;
+                float w = 1.f;
+                if (a.w && c < a.d) w = a.w[c];
+                xh[i][0] = in ? (xh[i][0] - mu) * r : 0.f;
+                gy[i][0] = in ? gy[i][0] : 0.f;
+                dw[i][0] = fmaf(gy[i][0], xh[i][0], dw[i][0]);
+                db[i][0] += gy[i][0];
+                gy[i][0] *= w;
+                a1[0] += gy[i][0];
+                a2[0] = fmaf(gy[i][0], xh[i][0], a2[0]);
             }
         }
+        float s1 = S == 2 ? a1[0] + a1[S - 1] : a1[0], s2 = S == 2 ? a2[0] + a2[S - 1] : a2[0];
         norm_group_sum<T>(s1, s2, red[odd]);
         const float m1 = s1 * inv_d, m2 = s2 * inv_d;
         if (!live || !a.out) continue;
@@ -280,8 +413,13 @@ __global__ void __launch_bounds__(NT) layer_norm_bwd_kernel(const __grid_constan
         for (int i = 0; i < NV; ++i) {
             const int c = (i * T + t) * VEC;
             if (c >= a.d) continue;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) gy[i][e] = r * (gy[i][e] - m1 - xh[i][e] * m2);
+            if constexpr (VEC == 8) {
+                norm_shift<VEC>(gy[i], -m1);
+                norm_fma<VEC>(gy[i], xh[i], -m2);
+                norm_scale<VEC>(gy[i], r);
+            } else {
+                gy[i][0] = r * (gy[i][0] - m1 - xh[i][0] * m2);
+            }
             norm_store_vec<VEC>(dx + c, gy[i]);
         }
     }

@@ -41,17 +41,16 @@ bool rows_aligned(const void* p, int32_t type, int64_t ld, int64_t n)
 // ------------------------------------------------------------- layer norm
 
 // CTAs of the backward pass with `threads` threads that take `groups` rows at once: as many as are
-// resident (1024 threads an SM: the rows held and read ahead take some 64 registers), fewer where
-// that leaves a CTA under 8 rows a group, since each CTA's partial sums (8 bytes a column) are
-// written and read once more.
+// resident, fewer where that leaves a CTA under 8 rows a group, since each CTA's partial sums (8 bytes
+// a column) are written and read once more.
 int32_t norm_bwd_ctas(int64_t n, int32_t groups, int32_t threads)
 {
-    const int64_t resident = int64_t(148) * (1024 / threads);
+    const int64_t resident = int64_t(148) * norm_bwd_per_sm(threads);
     return (int32_t)std::max<int64_t>(1, std::min((n + 8 * groups - 1) / (8 * groups), resident));
 }
 
 // The most CTAs any row group takes (narrow rows in groups of one warp or less: 256 threads).
-constexpr int64_t kNormMaxCtas = 148 * 8;
+constexpr int64_t kNormMaxCtas = 148 * norm_bwd_per_sm(128);
 
 template <typename TX, typename TY, int VEC, int T, int NV, int NT>
 dsa_status norm_launch(const NormArgs& a, bool backward, int32_t* n_part, cudaStream_t st)
@@ -125,18 +124,18 @@ size_t norm_ws_bytes(int64_t n, int32_t d)
 
 // ------------------------------------------------------------ distillation
 
-template <typename TT, int VEC, bool EDGE, int T, int NV, int NT>
+template <typename TT, bool WEIGHTS, int VEC, bool EDGE, int T, int NV, int NT>
 dsa_status distill_launch(const DistillArgs& a, cudaStream_t st)
 {
     constexpr int R = NT / T;
-    DSA_LAUNCH(kProfDistill, st, distill_kernel<TT, VEC, EDGE, T, NV, NT><<<(a.n + R - 1) / R, NT, 0, st>>>(a));
+    DSA_LAUNCH(kProfDistill, st, distill_kernel<TT, WEIGHTS, VEC, EDGE, T, NV, NT><<<(a.n + R - 1) / R, NT, 0, st>>>(a));
     return launched();
 }
 
-template <typename TT, bool EDGE, int NV, int NT, int CTAS = 1>
+template <typename TT, bool WEIGHTS, bool EDGE, int NV, int NT, int CTAS = 1>
 dsa_status distill_ring(const DistillArgs& a, cudaStream_t st)
 {
-    const auto kern = distill_ring_kernel<TT, EDGE, NV, NT, CTAS>;
+    const auto kern = distill_ring_kernel<TT, WEIGHTS, EDGE, NV, NT, CTAS>;
     const size_t smem = size_t(NV) * NT * (16 + 4 * sizeof(TT) + (a.list ? 16 : 0));
     dsa_status s = set_smem(kern, smem);
     if (s != DSA_OK) return s;
@@ -144,35 +143,42 @@ dsa_status distill_ring(const DistillArgs& a, cudaStream_t st)
     return launched();
 }
 
-template <typename TT, int VEC, bool EDGE>
+template <typename TT, bool WEIGHTS, int VEC, bool EDGE>
 dsa_status distill_pick(const DistillArgs& a, cudaStream_t st)
 {
     // 16 places a thread or so: with 8 the two joint reductions were a third of the instructions
     constexpr int U = 4 / VEC;   // registers' worth of a 4-wide load
     const int32_t k = EDGE ? a.k + 3 : a.k;   // columns from the boundary before the row
-    if (k <= 128) return distill_launch<TT, VEC, EDGE, 32, 1 * U, 256>(a, st);
-    if (k <= 512) return distill_launch<TT, VEC, EDGE, 32, 4 * U, 256>(a, st);
-    if (k <= 1024) return distill_launch<TT, VEC, EDGE, 64, 4 * U, 64>(a, st);
+    if (k <= 128) return distill_launch<TT, WEIGHTS, VEC, EDGE, 32, 1 * U, 256>(a, st);
+    if (k <= 512) return distill_launch<TT, WEIGHTS, VEC, EDGE, 32, 4 * U, 256>(a, st);
+    if (k <= 1024) return distill_launch<TT, WEIGHTS, VEC, EDGE, 64, 4 * U, 64>(a, st);
     // many rows: the next one read ahead, with as many CTAs an SM as hold rows of 64 KB together
     // (9765 x 2048: 51.9 us without, 43.5 with, fp32); not for rows off the 16-byte boundaries, whose
     // end vectors cost more there (9765 x 2049: 78 us without, 88 with)
     if constexpr (VEC == 4 && !EDGE) {
-        if (k > 1024 && k <= 2048 && a.n > 148 * 8) return distill_ring<TT, EDGE, 4, 128, 8>(a, st);
-        if (k > 2048 && k <= 4096 && a.n > 148 * 4) return distill_ring<TT, EDGE, 4, 256, 4>(a, st);
-        if (k > 4096 && k <= 8192 && a.n > 148 * 2) return distill_ring<TT, EDGE, 4, 512, 2>(a, st);
+        if (k > 1024 && k <= 2048 && a.n > 148 * 8) return distill_ring<TT, WEIGHTS, EDGE, 4, 128, 8>(a, st);
+        if (k > 2048 && k <= 4096 && a.n > 148 * 4) return distill_ring<TT, WEIGHTS, EDGE, 4, 256, 4>(a, st);
+        if (k > 4096 && k <= 8192 && a.n > 148 * 2) return distill_ring<TT, WEIGHTS, EDGE, 4, 512, 2>(a, st);
     }
-    if (k <= 2048) return distill_launch<TT, VEC, EDGE, 128, 4 * U, 128>(a, st);
-    if (k <= 4096) return distill_launch<TT, VEC, EDGE, 256, 4 * U, 256>(a, st);
-    if (k <= 8192) return distill_launch<TT, VEC, EDGE, 512, 4 * U, 512>(a, st);
+    if (k <= 2048) return distill_launch<TT, WEIGHTS, VEC, EDGE, 128, 4 * U, 128>(a, st);
+    if (k <= 4096) return distill_launch<TT, WEIGHTS, VEC, EDGE, 256, 4 * U, 256>(a, st);
+    if (k <= 8192) return distill_launch<TT, WEIGHTS, VEC, EDGE, 512, 4 * U, 512>(a, st);
     if constexpr (VEC == 4) {   // longer rows, as many as shared memory holds, read ahead
-        if (k <= 12288) return distill_ring<TT, EDGE, 6, 512>(a, st);
-        if (k <= 16384 && !a.list) return distill_ring<TT, EDGE, 8, 512>(a, st);
-        if (k <= 20480 && !a.list) return distill_ring<TT, EDGE, 10, 512>(a, st);
+        if (k <= 12288) return distill_ring<TT, WEIGHTS, EDGE, 6, 512>(a, st);
+        if (k <= 16384 && !a.list) return distill_ring<TT, WEIGHTS, EDGE, 8, 512>(a, st);
+        if (k <= 20480 && !a.list) return distill_ring<TT, WEIGHTS, EDGE, 10, 512>(a, st);
     }
-    if (k <= 16384) return distill_launch<TT, VEC, EDGE, 1024, 4 * U, 1024>(a, st);
-    if (k <= kDistillRegCols) return distill_launch<TT, VEC, EDGE, 1024, 5 * U, 1024>(a, st);
-    DSA_LAUNCH(kProfDistill, st, distill_long_kernel<TT, 512><<<a.n, 512, 0, st>>>(a));
+    if (k <= 16384) return distill_launch<TT, WEIGHTS, VEC, EDGE, 1024, 4 * U, 1024>(a, st);
+    if (k <= kDistillRegCols) return distill_launch<TT, WEIGHTS, VEC, EDGE, 1024, 5 * U, 1024>(a, st);
+    DSA_LAUNCH(kProfDistill, st, distill_long_kernel<TT, WEIGHTS, 512><<<a.n, 512, 0, st>>>(a));
     return launched();
+}
+
+template <typename TT, bool WEIGHTS>
+dsa_status distill_rows(const DistillArgs& a, bool vec, bool edge, cudaStream_t st)
+{
+    if (!vec) return distill_pick<TT, WEIGHTS, 1, false>(a, st);
+    return edge ? distill_pick<TT, WEIGHTS, 4, true>(a, st) : distill_pick<TT, WEIGHTS, 4, false>(a, st);
 }
 
 // ----------------------------------------------------- scores at listed keys
@@ -520,7 +526,6 @@ dsa_status dsa_distill_topk(int32_t n, int32_t k, const float* scores, int64_t l
     DistillArgs a{};
     a.s = scores; a.ld_s = ld_scores; a.list = lists; a.ld_list = ld_lists; a.t = teacher; a.ld_t = ld_teacher;
     a.g = grad_loss; a.loss = loss; a.ds = dscores; a.ld_ds = ld_dscores; a.n = n; a.k = k;
-    a.weights = teacher_kind == DSA_TEACHER_WEIGHTS ? 1 : 0;
     a.inv_tau = 1.f / temperature;
     a.scale = (float)(1.4426950408889634 / (double)temperature);
     // four places a load where the arrays' rows lie alike against 4-place boundaries
@@ -534,11 +539,11 @@ dsa_status dsa_distill_topk(int32_t n, int32_t k, const float* scores, int64_t l
                      alike(dscores, 4, ld_dscores);
     const bool edge = k % 4 != 0 || a.off0 != 0 || (n > 1 && a.off_step != 0);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool weights = teacher_kind == DSA_TEACHER_WEIGHTS;
     if (teacher_type == DSA_FP32)
-        return !vec ? distill_pick<float, 1, false>(a, st) : edge ? distill_pick<float, 4, true>(a, st)
-                                                                  : distill_pick<float, 4, false>(a, st);
-    return !vec ? distill_pick<__nv_bfloat16, 1, false>(a, st) : edge ? distill_pick<__nv_bfloat16, 4, true>(a, st)
-                                                                      : distill_pick<__nv_bfloat16, 4, false>(a, st);
+        return weights ? distill_rows<float, true>(a, vec, edge, st) : distill_rows<float, false>(a, vec, edge, st);
+    return weights ? distill_rows<__nv_bfloat16, true>(a, vec, edge, st)
+                   : distill_rows<__nv_bfloat16, false>(a, vec, edge, st);
 }
 
 // ----------------------------------------------------- scores at listed keys
