@@ -5,14 +5,22 @@
 //   S[128 keys x HP heads] = K_tile . Q^T                 (A = keys, B = heads, both K-major over d)
 //   scores: s[j] = sum_h w_h max(0, S[j,h])               (registers; one key per thread)
 //   backward, with e = ds[j]:
-//     G[j,h] = e w_h where S > 0, else 0, rounded to bf16 into shared memory,
+//     G[j,h] = e w_h where S > 0, else 0, in bf16 in shared memory,
 //     dQ^T[d x HP] += K_tile^T . G                        (both operands MN-major: the gathered tile and G as they lie)
 //     dW_h = sum_j e max(0, S[j,h])                       (fp32 registers, joined once per query)
-// The tile is read once for both products, so a query moves its listed keys from L2 exactly once;
-// that gather (256 bytes per listed pair at d = 128) is what bounds the kernel, not the products.
-// Roles: warp 0 and three late ones gather; warp 1 issues S, the last warp dQ; the warps between are
-// the epilogue.  S is double-buffered, so a tile's product runs while the tile before is worked on.
-// HP = max(16, H): heads above H have zero rows in the query tile.  Every wait is bounded.
+//     R[j] = G[j,:] . Q                                   (kListGradRows: rows that dK is summed from)
+// G is the one value rounded below fp32 (to the operands' type, once, after e w in fp32): independent
+// errors of 2^-9 that leave dQ and dK about 1.4 times their own rounding to bf16 off.
+//
+// What bounds it (d = 128, H = 64, 4096 queries of 2048 keys out of 32K):
+//   scores 250 us: the gather, 256 bytes a listed pair out of L2 at 8.4 TB/s (tensor pipe 25 %);
+//   dQ, dW 346 us: shared memory, of whose bandwidth a tile of 128 keys takes 1150 of 1450 clocks (32 KB
+//     gathered, 48 KB read by S, 48 KB by dQ, 16 KB of G written); tensor pipe 36 %, issue 58 %;
+//   with rows 1146 us: 512 bytes a pair written, 3.7 TB/s.
+// Roles: warp 0 and three late ones gather; warp 1 issues S, a late one dQ (and R); the warps between are
+// the epilogue, the last eight (kListGradRows) store R.  S is double-buffered, so a tile's product runs
+// while the tile before is worked on.  HP = max(16, H): heads above H have zero rows in the query tile.
+// Every wait is bounded.
 #pragma once
 
 #include <math_constants.h>
@@ -23,8 +31,8 @@
 namespace dsa {
 
 // Epilogue warps: two groups on alternate tiles, of four warps (forward) or of eight (backward: two sets,
-// half of the heads each).  Measured backward, 4096 queries x 2048 keys, H = 64: 64 heads a thread in two
-// groups 556 us, 16 heads a thread in one group 322 us (both with one issuer's other steps alike).
+// half of the heads each).  Backward measured 421 us for a packed batch of 8K queries with 16 heads a
+// thread in one group, 400 us so (and 373 with the other steps since).
 constexpr int kListTcProducers = 4;
 constexpr int list_sets(int mode) { return mode ? 4 : 2; }
 constexpr int list_threads(int mode)
@@ -329,7 +337,7 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
     if (warp == 0 || (warp >= 2 + kEpi && warp < 5 + kEpi)) {
         // ------------------------------------------------------ producers
         // Four warps of 32 tile rows each, 16 bytes a lane (asynchronous copies, two rows of 256 bytes
-        // an instruction at d = 128).  Gathering the same tile with TMA (gather4) took 2400 clocks.
+        // an instruction at d = 128): 1050 clocks a tile, the L2's pace; TMA (gather4) took 2400.
         const int pw = warp == 0 ? 0 : warp - 1 - kEpi;
         constexpr int CPR = D / 8;             // 16-byte chunks of a row
         constexpr int RPI = 32 / CPR;          // rows per instruction
