@@ -15,7 +15,10 @@
 
 namespace dsa {
 
-// bits[w][n_k]: bit b of word w of key row s: query t0 + 32 w + b lists it.  One warp per query.
+constexpr int kBitsPlaces = 512;   // list places of a warp of the marking kernel
+
+// bits[w][n_k]: bit b of word w of key row s: query t0 + 32 w + b lists it.  A warp per kBitsPlaces places
+// of a query (blockIdx.y: which).
 __global__ void __launch_bounds__(256) list_bits_kernel(const int32_t* lists, int32_t k, const RowDesc* rows,
                                                         const int32_t* k_off, int32_t t0, int32_t t1, int32_t n_k,
                                                         uint32_t* bits, uint32_t* status)
@@ -23,12 +26,13 @@ __global__ void __launch_bounds__(256) list_bits_kernel(const int32_t* lists, in
     const int t = t0 + blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (t >= t1) return;
     const RowDesc r = rows[t];
+    const int i0 = blockIdx.y * kBitsPlaces, i1 = min(r.ncols, i0 + kBitsPlaces);
     const int32_t* l = lists + (int64_t)t * k;
     uint32_t* word = bits + (int64_t)((t - t0) >> 5) * n_k;
     const uint32_t bit = 1u << ((t - t0) & 31);
     const int kb = k_off[r.seq];
 #pragma unroll 8
-    for (int i = lane; i < r.ncols; i += 32) {
+    for (int i = i0 + lane; i < i1; i += 32) {
         const int s = kb + __ldg(l + i);
         if (DSA_CHECK(s >= 0 && s < n_k, status, 117)) atomicOr(word + s, bit);
     }
@@ -67,10 +71,16 @@ __global__ void __launch_bounds__(kPosBlock) list_count_kernel(const uint32_t* b
     const int s = blockIdx.x * kPosBlock + threadIdx.x;
     uint32_t n = 0;
     if (s < n_k) {
-#pragma unroll 8
-        for (int w = 0; w < words; ++w) {
-            pre[(int64_t)w * n_k + s] = (uint16_t)n;
-            n += __popc(bits[(int64_t)w * n_k + s]);
+        constexpr int U = 16;   // words read together
+        for (int w0 = 0; w0 < words; w0 += U) {
+            uint32_t b[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) b[u] = w0 + u < words ? bits[(int64_t)(w0 + u) * n_k + s] : 0u;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (w0 + u < words) pre[(int64_t)(w0 + u) * n_k + s] = (uint16_t)n;
+                n += __popc(b[u]);
+            }
         }
         count[s] = n;
     }

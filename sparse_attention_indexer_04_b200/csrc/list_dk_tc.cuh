@@ -391,10 +391,16 @@ __global__ void __launch_bounds__(256) list_dk_join_kernel(const float4* part, i
 {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n4) return;
-    float4 s = part[i];
-    for (int p = 1; p < parts; ++p) {
-        const float4 v = part[p * n4 + i];
-        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int U = 8;   // parts read together
+    for (int p0 = 0; p0 < parts; p0 += U) {
+        float4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = p0 + u < parts ? part[(p0 + u) * n4 + i] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            s.x += v[u].x; s.y += v[u].y; s.z += v[u].z; s.w += v[u].w;
+        }
     }
     dK[i] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
 }

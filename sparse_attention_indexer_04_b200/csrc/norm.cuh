@@ -477,9 +477,15 @@ __global__ void __launch_bounds__(1024) layer_norm_dw_kernel(const float* part, 
     const int c = blockIdx.x * 32 + tx;
     grid_dep_wait();
     float s = 0.f;
+    constexpr int U = 8;   // rows read together
     if (c < 2 * d)
-#pragma unroll 8
-        for (int i = ty; i < n_part; i += 32) s += part[(int64_t)i * 2 * d + c];
+        for (int i0 = ty; i0 < n_part; i0 += 32 * U) {
+            float v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = i0 + 32 * u < n_part ? part[(int64_t)(i0 + 32 * u) * 2 * d + c] : 0.f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) s += v[u];
+        }
     sh[ty][tx] = s;
     __syncthreads();
     if (ty == 0 && c < 2 * d) {

@@ -420,8 +420,9 @@ dsa_status list_backward_d(const ListArgs& a, const ListPlan& p, cudaStream_t st
         const int32_t t1 = std::min(t0 + p.chunk, a.n_q), words = (t1 - t0 + 31) / 32;
         const int32_t blocks = (a.n_k + kPosBlock - 1) / kPosBlock;
         if (cudaMemsetAsync(p.bits, 0, size_t(words) * a.n_k * 4, st) != cudaSuccess) return DSA_ERR_CUDA;
-        DSA_LAUNCH(kProfSetup, st, list_bits_kernel<<<(t1 - t0 + 7) / 8, 256, 0, st>>>(a.lists, a.k, a.rows, a.k_off, t0, t1,
-                                                                                       a.n_k, p.bits, a.status));
+        const dim3 marks((t1 - t0 + 7) / 8, (a.k + kBitsPlaces - 1) / kBitsPlaces);
+        DSA_LAUNCH(kProfSetup, st, list_bits_kernel<<<marks, 256, 0, st>>>(a.lists, a.k, a.rows, a.k_off, t0, t1, a.n_k,
+                                                                           p.bits, a.status));
         DSA_LAUNCH(kProfSetup, st, list_count_kernel<<<blocks, kPosBlock, 0, st>>>(p.bits, words, a.n_k, p.pre, p.count,
                                                                                   p.off, p.base));
         DSA_LAUNCH(kProfSetup, st, list_base_kernel<<<1, 1024, 0, st>>>(p.base, blocks));
