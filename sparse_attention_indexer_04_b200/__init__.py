@@ -17,6 +17,7 @@ Entry points mirror include/dsa_index.h:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -436,6 +437,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, out_dtype
     return (out, mean, rstd) if want_stats else out
 
 
+@functools.lru_cache(maxsize=256)
 def layer_norm_backward_workspace(n: int, d: int) -> int:
     return int(_lib.dsa_layer_norm_backward_workspace(n, d))
 

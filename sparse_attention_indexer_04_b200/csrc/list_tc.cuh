@@ -581,6 +581,36 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
         bool alive = true;
         RowDesc nx = t0 < n_q ? a.l.rows[t0] : none;
         float wnext = st < H && t0 < n_q ? a.l.W[(int64_t)t0 * H + st] : 0.f;
+        // With few heads dQ of a query is read a query later, when its last product has long been made
+        // (4096 queries of 512 keys, H = 4: 82 us at once, 74 so; with 64 heads the registers that it
+        // takes cost more than the wait: 373 us at once, 403 so)
+        constexpr bool LATE = HP < 64;
+        [[maybe_unused]] int held = -1;
+        [[maybe_unused]] auto readout = [&](int t, int i) {   // query t, the i-th with a list
+            constexpr int NR = HP / 4;     // heads whose dQ a set writes
+            const int r0 = set * NR, qb = i & 1;
+            alive = tc_wait_warp(&dqfull[qb], (i >> 1) & 1, status, 33, abort_flag, alive);
+            if (!alive) return;
+            tc_fence_after();
+            float v[NR];
+            tmem_load<NR>(tDQ + qb * 64 + r0 + lanes, v);
+            tc_fence_before();
+            mbar_arrive(&dqfree[qb]);
+            if (a.l.dQ && lrow < D) {
+                __nv_bfloat16* out = a.l.dQ + ((int64_t)t * H + r0) * D + lrow;
+#pragma unroll
+                for (int c = 0; c < NR; ++c)
+                    if (r0 + c < H) out[c * D] = __float2bfloat16_rn(v[c]);
+            }
+            __syncwarp();
+        };
+        // ds of a query's first tile of this set's group
+        [[maybe_unused]] float first = 0.f;
+        [[maybe_unused]] auto ask = [&](int t, int n, int ncols) {
+            const int j = ((n & 1) == (set >> 1) ? 0 : 128) + lrow;
+            first = t < n_q && j < ncols ? a.l.ds[(int64_t)t * k + j] : 0.f;
+        };
+        if (BWD) ask(t0, 0, nx.ncols);
         for (int t = t0; t < n_q; t += step, ++all) {
             const RowDesc r = nx;
             float* w = sW + (set * 2 + (all & 1)) * HP;
@@ -623,7 +653,7 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
                 for (int h = 0; h < NC / 2; ++h) dw[h] = 0;
                 const float* ds = a.l.ds + (int64_t)t * k + lrow;
                 int i = (n & 1) == grp ? 0 : 1;   // the group's first tile
-                float e = i * 128 + lrow < r.ncols ? ds[i * 128] : 0.f;
+                float e = first;
                 for (; i < nt; i += 2) {
                     const uint32_t use = (uint32_t)((n + i) >> 1) & 1u;
                     // a place behind the list's end repeats the last key: its products count for nothing (e = 0)
@@ -662,6 +692,7 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     mbar_arrive(&gfull[grp]);
                 }
+                ask(t + step, n + nt, nx.ncols);   // under the joining of dW
                 float dv[NC];
 #pragma unroll
                 for (int h = 0; h < NC / 2; ++h) unpack_f32x2(dw[h], dv[2 * h], dv[2 * h + 1]);
@@ -676,24 +707,12 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
                     for (int x = 0; x < 8; ++x) s += part[x * HP + h];
                     a.l.dW[(int64_t)t * H + h] = s;
                 }
-                constexpr int NR = HP / 4;     // heads whose dQ a set writes
-                const int r0 = set * NR;
                 if (nt > 0) {
-                    const int qb = it & 1;
-                    alive = tc_wait_warp(&dqfull[qb], (it >> 1) & 1, status, 33, abort_flag, alive);
-                    if (alive) {
-                        tc_fence_after();
-                        float v[NR];
-                        tmem_load<NR>(tDQ + qb * 64 + r0 + lanes, v);
-                        tc_fence_before();
-                        mbar_arrive(&dqfree[qb]);
-                        if (a.l.dQ && lrow < D) {
-                            __nv_bfloat16* out = a.l.dQ + ((int64_t)t * H + r0) * D + lrow;
-#pragma unroll
-                            for (int c = 0; c < NR; ++c)
-                                if (r0 + c < H) out[c * D] = __float2bfloat16_rn(v[c]);
-                        }
-                        __syncwarp();
+                    if (!LATE) {
+                        readout(t, it);
+                    } else {
+                        if (held >= 0) readout(held, it - 1);
+                        held = t;
                     }
                 } else if (a.l.dQ) {   // nothing listed: zero gradients
                     for (int o = threadIdx.x - 64; o < H * D; o += 512)
@@ -703,6 +722,7 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
             n += nt;
             if (nt > 0) ++it;
         }
+        if (BWD && LATE && held >= 0) readout(held, it - 1);
     }
 
     tc_fence_before();

@@ -236,22 +236,24 @@ ListWork list_work(const dsa_batch* b, int32_t k)
 }
 
 // Whether dK is summed from one row per listed pair or from dense products over whole key blocks.
-// Measured at d = 128: a row 0.22 ns (written by the dQ pass, read once), a (query, block) product 6.8 ns
-// with 64 heads, 2.5 with 8, 1.2 with 4.
+// Measured at d = 128, in ns: a row 0.22 (written by the dQ pass, read once), a key 0.16 and four more
+// launches 15,000; a (query, block) product 6.8 with 64 heads, 2.5 with 8, 1.2 with 4, a block's CTA 70.
 bool dk_by_rows(const dsa_batch* b, int32_t k)
 {
     const ListWork w = list_work(b, k);
-    return w.listed * 0.22 < w.blocks * (1.2 + 5.6 * b->num_heads / 64.);
+    const double units = b->num_keys / kDkKeys + b->num_seqs;
+    return w.listed * 0.22 + b->num_keys * 0.16 + 15000 < w.blocks * (1.2 + 5.6 * b->num_heads / 64.) + units * 70;
 }
 
 // Whether the listed scores are picked from all scores of the prefix or computed from gathered keys.
-// Measured at d = 128: a gathered pair 33 ps, a dense one 14 ps with 64 heads, and 2 ps to write and read it.
+// Measured at d = 128, in ns: a gathered pair 0.033; a dense one 0.014 with 64 heads and 0.002 to write and
+// read it, two more launches 8000.
 bool scores_by_picking(const dsa_batch* b, const HostInfo& hi, int32_t k)
 {
     if (size_t(b->num_queries) * dense_scores_ld(hi.max_k) * 4 > (size_t(4) << 30)) return false;
     const ListWork w = list_work(b, k);
     const double d = b->head_dim / 128.;
-    return w.dense * (2 + 14 * d * b->num_heads / 64.) < w.listed * 33 * d;
+    return w.dense * (0.002 + 0.014 * d * b->num_heads / 64.) + 8000 < w.listed * 0.033 * d;
 }
 
 // CTAs that share a key block's queries: enough for three waves over the GPU (a block's work is its
