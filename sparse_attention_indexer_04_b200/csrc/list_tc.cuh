@@ -350,16 +350,29 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
         uint32_t phase = 0;
         int q_issued = 0;
         bool alive = true;
-        RowDesc nx = t0 < n_q ? a.l.rows[t0] : none;
+        // rows two queries ahead; the next query's first keys and its sequence's first key row one ahead, so
+        // that queries of one tile do not wait for them in turn
+        RowDesc nx = t0 < n_q ? a.l.rows[t0] : none, nx2 = t0 + step < n_q ? a.l.rows[t0 + step] : none;
+        int key_next = 0, kb_next = 0;
+        auto ask = [&](int t, const RowDesc& r) {
+            if (t >= n_q || r.ncols == 0) return;
+            // places behind the last take its key again
+            key_next = __ldg(a.l.lists + (int64_t)t * k + min(pw * 32 + lane, r.ncols - 1));
+            kb_next = a.l.k_off[r.seq];
+        };
+        ask(t0, nx);
         for (int t = t0; t < n_q && alive; t += step) {
             const RowDesc r = nx;
-            if (t + step < n_q) nx = a.l.rows[t + step];
+            nx = nx2;
+            if (t + 2 * step < n_q) nx2 = a.l.rows[t + 2 * step];
+            int key = key_next;
+            const int kb = kb_next;
+            ask(t + step, nx);
             const int nt = (r.ncols + 127) >> 7;
             if (nt == 0) continue;
             const int qb = it & 1;
             const int32_t* l = a.l.lists + (int64_t)t * k + pw * 32 + lane;
-            const int last = r.ncols - 1 - pw * 32 - lane;   // places behind the last take its key again
-            int key = __ldg(l + min(0, last));
+            const int last = r.ncols - 1 - pw * 32 - lane;
             if (pw == 0) {
                 int ok = 1;
                 if (lane == 0) {
@@ -374,7 +387,7 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
                 ++q_issued;
             }
             ++it;
-            const __nv_bfloat16* kbase = a.l.K + (int64_t)a.l.k_off[r.seq] * D + chunk * 8;
+            const __nv_bfloat16* kbase = a.l.K + (int64_t)kb * D + chunk * 8;
             [[maybe_unused]] const int n_seq = a.l.k_off[r.seq + 1] - a.l.k_off[r.seq];
             for (int i = 0; i < nt; ++i) {
                 const int mine = DSA_CHECK(key >= 0 && key < n_seq, status, 113) ? key : 0;
@@ -411,10 +424,11 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
         uint32_t phase = 0;
         int n = 0, it = 0;     // tiles and non-empty queries so far
         bool alive = true;
-        int nx = t0 < n_q ? a.l.rows[t0].ncols : 0;
+        int nx = t0 < n_q ? a.l.rows[t0].ncols : 0, nx2 = t0 + step < n_q ? a.l.rows[t0 + step].ncols : 0;
         for (int t = t0; t < n_q && alive; t += step) {
             const int nt = __shfl_sync(0xffffffffu, (nx + 127) >> 7, 0);
-            if (t + step < n_q) nx = a.l.rows[t + step].ncols;
+            nx = nx2;
+            if (t + 2 * step < n_q) nx2 = a.l.rows[t + 2 * step].ncols;
             if (nt == 0) continue;
             const int qb = it & 1;
             alive = tc_wait_warp(&qfull[qb], (it >> 1) & 1, status, 27, abort_flag, alive);
@@ -460,10 +474,11 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
         const uint32_t tbase = __shfl_sync(0xffffffffu, tmem, 0) + 128;
         int stage = 0, n = 0, it = 0;
         bool alive = true;
-        int nx = t0 < n_q ? a.l.rows[t0].ncols : 0;
+        int nx = t0 < n_q ? a.l.rows[t0].ncols : 0, nx2 = t0 + step < n_q ? a.l.rows[t0 + step].ncols : 0;
         for (int t = t0; t < n_q && alive; t += step) {
             const int nt = __shfl_sync(0xffffffffu, (nx + 127) >> 7, 0);
-            if (t + step < n_q) nx = a.l.rows[t + step].ncols;
+            nx = nx2;
+            if (t + 2 * step < n_q) nx2 = a.l.rows[t + 2 * step].ncols;
             if (nt == 0) continue;
             const int qb = it & 1;
             alive = tc_wait_warp(&dqfree[qb], ((it >> 1) & 1) ^ 1u, status, 26, abort_flag, alive);
@@ -579,7 +594,7 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         int n = 0, it = 0, all = 0;
         bool alive = true;
-        RowDesc nx = t0 < n_q ? a.l.rows[t0] : none;
+        int nx = t0 < n_q ? a.l.rows[t0].ncols : 0, nx2 = t0 + step < n_q ? a.l.rows[t0 + step].ncols : 0;
         float wnext = st < H && t0 < n_q ? a.l.W[(int64_t)t0 * H + st] : 0.f;
         // With few heads dQ of a query is read a query later, when its last product has long been made
         // (4096 queries of 512 keys, H = 4: 82 us at once, 74 so; with 64 heads the registers that it
@@ -610,17 +625,16 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
             const int j = ((n & 1) == (set >> 1) ? 0 : 128) + lrow;
             first = t < n_q && j < ncols ? a.l.ds[(int64_t)t * k + j] : 0.f;
         };
-        if (BWD) ask(t0, 0, nx.ncols);
+        if (BWD) ask(t0, 0, nx);
         for (int t = t0; t < n_q; t += step, ++all) {
-            const RowDesc r = nx;
+            const int ncols = nx;
+            nx = nx2;
+            if (t + 2 * step < n_q) nx2 = a.l.rows[t + 2 * step].ncols;
             float* w = sW + (set * 2 + (all & 1)) * HP;
             if (st < HP) w[st] = wnext;
-            if (t + step < n_q) {
-                nx = a.l.rows[t + step];
-                wnext = st < H ? a.l.W[(int64_t)(t + step) * H + st] : 0.f;
-            }
+            if (t + step < n_q) wnext = st < H ? a.l.W[(int64_t)(t + step) * H + st] : 0.f;
             named_barrier(1 + set, 128);
-            const int nt = (r.ncols + 127) >> 7;
+            const int nt = (ncols + 127) >> 7;
             if constexpr (!BWD) {
                 for (int i = (n & 1) == set ? 0 : 1; i < nt; i += 2) {   // the set's tiles
                     const int g = n + i;   // the CTA's tile number
@@ -641,7 +655,7 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
                     }
                     float s0, s1;
                     unpack_f32x2(acc, s0, s1);
-                    if (j < k) a.l.scores[(int64_t)t * k + j] = j < r.ncols ? (s0 + s1) + 0.f : -CUDART_INF_F;
+                    if (j < k) a.l.scores[(int64_t)t * k + j] = j < ncols ? (s0 + s1) + 0.f : -CUDART_INF_F;
                 }
                 if (set == 0)   // places behind the last tile
                     for (int j = nt * 128 + st; j < k; j += 128) a.l.scores[(int64_t)t * k + j] = -CUDART_INF_F;
@@ -658,7 +672,7 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
                     const uint32_t use = (uint32_t)((n + i) >> 1) & 1u;
                     // a place behind the list's end repeats the last key: its products count for nothing (e = 0)
                     const uint64_t ee = pack_f32x2(e, e);
-                    e = (i + 2) * 128 + lrow < r.ncols ? ds[(i + 2) * 128] : 0.f;
+                    e = (i + 2) * 128 + lrow < ncols ? ds[(i + 2) * 128] : 0.f;
                     alive = tc_wait_warp(&sfull[grp], use, status, 31, abort_flag, alive);
                     alive = tc_wait_warp(&gfree[grp], use ^ 1u, status, 32, abort_flag, alive);
                     if (!alive) continue;
@@ -692,7 +706,7 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     mbar_arrive(&gfull[grp]);
                 }
-                ask(t + step, n + nt, nx.ncols);   // under the joining of dW
+                ask(t + step, n + nt, nx);   // under the joining of dW
                 float dv[NC];
 #pragma unroll
                 for (int h = 0; h < NC / 2; ++h) unpack_f32x2(dw[h], dv[2 * h], dv[2 * h + 1]);
