@@ -333,7 +333,9 @@ dsa_status dsa_distill_topk(int32_t n, int32_t k, const float* scores, int64_t l
  * not ascending, holds a key outside its sequence or has a key after its
  * padding is used up to its first bad entry and reported through the
  * workspace status word (code 2, read with dsa_device_check).
- * Requires 1 <= k <= 16384.
+ * Requires 1 <= k <= 16384.  The listed keys are gathered, or, where lists
+ * cover much of their prefixes, picked from all its scores (at most 4 GiB of
+ * the workspace); the choice depends on the sizes alone.
  */
 size_t dsa_list_scores_workspace(const dsa_batch* batch, int32_t k);
 dsa_status dsa_list_scores(const dsa_batch* batch, const void* Q, const void* K, const float* W, int32_t k,
@@ -346,7 +348,10 @@ dsa_status dsa_list_scores(const dsa_batch* batch, const void* Q, const void* K,
  *     dW[t,h] = sum_j dscores[t,j] max(0, q[t,h] . k),
  *     G = dscores[t,j] w[t,h] where q[t,h] . k > 0 (else 0),
  *     dQ[t,h] = sum_j G k,   dK[s] = sum over the (t, h) that list s of G q[t,h].
- * dQ and dK 16-byte aligned.
+ * G is rounded to bf16 once (an operand beside Q and K); everything else is
+ * fp32 until the outputs are rounded.  dQ and dK 16-byte aligned.  The
+ * workspace holds partial sums of dK or, where lists cover little of their
+ * prefixes, its rows: up to some GiB for large batches.
  */
 size_t dsa_list_scores_backward_workspace(const dsa_batch* batch, int32_t k);
 dsa_status dsa_list_scores_backward(const dsa_batch* batch, const void* Q, const void* K, const float* W, int32_t k,

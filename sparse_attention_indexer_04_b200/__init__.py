@@ -418,6 +418,15 @@ def _on(index, call, *args, stream=None):
     return call(*args, raw)
 
 
+def _used_on(stream, *made):
+    """Tells the allocator that tensors made here on the current stream are in use on `stream`: their memory is
+    not handed out again before that stream's work so far is done."""
+    if stream is not None:
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, out_dtype=None, want_stats=False, stream=None):
     """Layer norm of the rows of x [n, d] (bf16 or fp32; rows may be a slice of a wider matrix): y [n, d] of
     out_dtype (x's by default); with want_stats also mean and rstd [n] fp32, which the backward pass takes."""
@@ -434,6 +443,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, out_dtype
         mp, rp = mean.data_ptr(), rstd.data_ptr()
     _check(_on(dev, _lib.dsa_layer_norm, n, d, x.data_ptr(), _TYPES[x.dtype], ld_x, w, b, eps, out.data_ptr(),
                _TYPES[out.dtype], ld_y, mp, rp, stream=stream), "dsa_layer_norm")
+    _used_on(stream, out, mean, rstd)
     return (out, mean, rstd) if want_stats else out
 
 
@@ -459,6 +469,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, dx=None, ws=None, stream=None
     _check(_on(dev, _lib.dsa_layer_norm_backward, n, d, dy.data_ptr(), _TYPES[dy.dtype], ld_dy, x.data_ptr(),
                _TYPES[x.dtype], ld_x, w, mp, rp, dx.data_ptr(), ld_dx, dw.data_ptr(), db.data_ptr(), ws.data_ptr(),
                ws.numel() * ws.element_size(), stream=stream), "dsa_layer_norm_backward")
+    _used_on(stream, dx, dw, db, ws)
     return dx, dw, db
 
 
@@ -481,6 +492,7 @@ def distill_topk(scores, teacher, lists=None, kind: int = TEACHER_LOGITS, temper
     _check(_on(dev, _lib.dsa_distill_topk, n, k, scores.data_ptr(), ld_s, lp, ld_l, teacher.data_ptr(),
                _TYPES[teacher.dtype], ld_t, kind, temperature, g, _dense(loss, "loss", dev, (n,), torch.float32),
                dscores.data_ptr(), ld_d, stream=stream), "dsa_distill_topk")
+    _used_on(stream, loss, dscores)
     return loss, dscores
 
 
@@ -514,6 +526,7 @@ def list_scores(layout: Layout, Q, K, W, lists, scores=None, ws=None, stream=Non
     _check(_on(dev, _lib.dsa_list_scores, layout.ref(), q, kk, w, k, l,
                _dense(scores, "scores", dev, lists.shape, torch.float32), ws.data_ptr(), ws.numel() * ws.element_size(),
                stream=stream), "dsa_list_scores")
+    _used_on(stream, scores, ws)
     _after(ws, "dsa_list_scores", stream)
     return scores
 
@@ -535,6 +548,7 @@ def list_scores_backward(layout: Layout, Q, K, W, lists, dscores, dQ=None, dK=No
                _dense(dQ, "dQ", dev, Q.shape, torch.bfloat16), _dense(dK, "dK", dev, K.shape, torch.bfloat16),
                _dense(dW, "dW", dev, W.shape, torch.float32), ws.data_ptr(), ws.numel() * ws.element_size(),
                stream=stream), "dsa_list_scores_backward")
+    _used_on(stream, dQ, dK, dW, ws)
     _after(ws, "dsa_list_scores_backward", stream)
     return dQ, dK, dW
 

@@ -539,6 +539,31 @@ def test_an_explicit_stream_is_used():
     assert torch.equal(y, want)
 
 
+def test_memory_made_for_another_stream_is_not_handed_out_early():
+    """A call on a stream of its own makes its workspace and outputs on the current stream; work queued there
+    afterwards, which the allocator serves from freed memory, must not reach them while the call still runs."""
+    b = workloads.ragged(96, [300, 200], [300, 900], H=64, d=128, k=64, integer=False)
+    lay, Q, K, W = on_gpu(b)
+    g = gen(96)
+    lists, ds = random_lists(g, b, 64).to(DEV), randn(g, b.n_q, 64).to(DEV)
+    want = dsa.list_scores_backward(lay, Q, K, W, lists, ds)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream(DEV)
+    size = dsa.list_scores_backward_workspace(lay, 64)
+    busy = torch.randn(4096, 4096, device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(st):
+            for _ in range(4):
+                busy @ busy              # keeps the stream behind the host
+        got = dsa.list_scores_backward(lay, Q, K, W, lists, ds, stream=st)
+        junk = torch.full((size,), 255, dtype=torch.uint8, device=DEV)
+        torch.cuda.synchronize()
+        for u, v in zip(want, got):
+            assert torch.equal(u, v)
+        del junk
+
+
 def test_binding_refuses_what_the_library_cannot_read():
     x = torch.zeros(8, 16, device=DEV)
     for bad in (lambda: dsa.layer_norm(x.half()), lambda: dsa.layer_norm(x.t()), lambda: dsa.layer_norm(x[0]),
