@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32) list_dk_rows_kernel(const __g
 {
     constexpr int V = D / 32;   // columns of a lane
     const int lane = threadIdx.x & 31, s = blockIdx.x * kRowsWarps + (threadIdx.x >> 5);
+    grid_dep_wait();
     if (s >= a.n_k) return;
     const int n = a.count[s];
     if (n == 0 && !a.first && !a.last) return;

@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(kDkThreads, 1)
         prefetch_tensormap(&tmK);
     }
     if (warp == 4) tmem_alloc(tmem_slot, 512);
+    grid_dep_wait();   // the edges and lists' lengths come from earlier kernels
 
     // the part's queries that list a key of the block, in order (query part + ordinal * parts)
     const uint16_t* e0 = a.edge + (int64_t)blk * a.l.n_q + q0;
@@ -390,6 +391,7 @@ __global__ void __launch_bounds__(kDkThreads, 1)
 __global__ void __launch_bounds__(256) list_dk_join_kernel(const float4* part, int32_t parts, int64_t n4, uint2* dK)
 {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    grid_dep_wait();
     if (i >= n4) return;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int U = 8;   // parts read together

@@ -385,11 +385,12 @@ dsa_status list_dk_launch(const ListArgs& l, const ListPlan& p, cudaStream_t st)
     const int smem = std::max<int>(SH::bytes, 120 * 1024);   // one CTA an SM: each takes all of TMEM
     dsa_status s = set_smem(list_dk_tc_kernel<D, H>, smem);
     if (s != DSA_OK) return s;
-    DSA_LAUNCH(kProfListDk, st, list_dk_tc_kernel<D, H><<<(unsigned)p.units * p.parts, kDkThreads, smem, st>>>(mk, a));
+    DSA_LAUNCH(kProfListDk, st, launch_pdl(true, list_dk_tc_kernel<D, H>, (unsigned)p.units * p.parts, kDkThreads, smem, st, mk, a));
     if ((s = launched()) != DSA_OK || p.parts == 1) return s;
     const int64_t n4 = int64_t(l.n_k) * D / 4;
-    DSA_LAUNCH(kProfListDk, st, list_dk_join_kernel<<<(unsigned)((n4 + 255) / 256), 256, 0, st>>>(
-        reinterpret_cast<const float4*>(p.part), p.parts, n4, reinterpret_cast<uint2*>(l.dK)));
+    DSA_LAUNCH(kProfListDk, st, launch_pdl(true, list_dk_join_kernel, (unsigned)((n4 + 255) / 256), 256, 0, st,
+                                           reinterpret_cast<const float4*>(p.part), p.parts, n4,
+                                           reinterpret_cast<uint2*>(l.dK)));
     return launched();
 }
 
@@ -431,8 +432,8 @@ dsa_status list_backward_d(const ListArgs& a, const ListPlan& p, cudaStream_t st
         if ((s = launched()) != DSA_OK) return s;
         if ((s = list_tc<D, kListGradRows>(a, t0, t1, p, st)) != DSA_OK) return s;
         const DkRowsArgs r{p.part, p.count, p.off, p.base, p.acc, a.dK, a.n_k, t0 == 0, t1 == a.n_q};
-        DSA_LAUNCH(kProfListDk, st, list_dk_rows_kernel<D>
-                   <<<(a.n_k + kRowsWarps - 1) / kRowsWarps, kRowsWarps * 32, 0, st>>>(r));
+        DSA_LAUNCH(kProfListDk, st, launch_pdl(true, list_dk_rows_kernel<D>, (a.n_k + kRowsWarps - 1) / kRowsWarps,
+                                               kRowsWarps * 32, 0, st, r));
         if ((s = launched()) != DSA_OK) return s;
     }
     return DSA_OK;
