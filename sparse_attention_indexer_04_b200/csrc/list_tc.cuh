@@ -213,6 +213,7 @@ struct ListTcArgs {
     ListArgs l;
     int32_t n_stages;
     int32_t t0, t1;        // queries of the launch
+    int32_t splits;        // kListScores: CTAs of a query, which take its tiles in turn (1: every CTA several queries)
     // kListGradRows: the rows sum_h G[t,j,h] q[t,h], stored by key.  Key row s lists its rows from
     // base[s / keys of a block] + off[s] on; before query t's come pre + the bits below t's.
     float* part;
@@ -331,7 +332,13 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t tS = tmem, tDQ = tmem + 128;
-    const int t0 = a.t0 + blockIdx.x, n_q = a.t1, H = a.l.H, k = a.l.k, step = gridDim.x;
+    const int P = BWD ? 1 : a.splits, p = BWD ? 0 : blockIdx.x % P;
+    const int t0 = a.t0 + blockIdx.x / P, n_q = a.t1, H = a.l.H, k = a.l.k, step = gridDim.x / P;
+    // this CTA's tiles of a list: p, p + P, ...
+    auto tiles = [&](int ncols) {
+        const int nt = (ncols + 127) >> 7;
+        return BWD ? nt : nt > p ? (nt - p + P - 1) / P : 0;
+    };
     const RowDesc none{0, 0, 0, 0};
 
     if (warp == 0 || (warp >= 2 + kEpi && warp < 5 + kEpi)) {
@@ -357,7 +364,7 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
         auto ask = [&](int t, const RowDesc& r) {
             if (t >= n_q || r.ncols == 0) return;
             // places behind the last take its key again
-            key_next = __ldg(a.l.lists + (int64_t)t * k + min(pw * 32 + lane, r.ncols - 1));
+            key_next = __ldg(a.l.lists + (int64_t)t * k + min(p * 128 + pw * 32 + lane, r.ncols - 1));
             kb_next = a.l.k_off[r.seq];
         };
         ask(t0, nx);
@@ -368,7 +375,7 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
             int key = key_next;
             const int kb = kb_next;
             ask(t + step, nx);
-            const int nt = (r.ncols + 127) >> 7;
+            const int nt = tiles(r.ncols);
             if (nt == 0) continue;
             const int qb = it & 1;
             const int32_t* l = a.l.lists + (int64_t)t * k + pw * 32 + lane;
@@ -391,7 +398,7 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
             [[maybe_unused]] const int n_seq = a.l.k_off[r.seq + 1] - a.l.k_off[r.seq];
             for (int i = 0; i < nt; ++i) {
                 const int mine = DSA_CHECK(key >= 0 && key < n_seq, status, 113) ? key : 0;
-                if (i + 1 < nt) key = __ldg(l + min((i + 1) * 128, last));
+                if (i + 1 < nt) key = __ldg(l + min((p + (i + 1) * P) * 128, last));
                 alive = tc_wait_warp(&kempty[stage], phase ^ 1u, status, 22, abort_flag, alive);
                 if (!alive) break;
                 const uint32_t tile = sk + stage * SH::KTILE + coff;
@@ -426,7 +433,7 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
         bool alive = true;
         int nx = t0 < n_q ? a.l.rows[t0].ncols : 0, nx2 = t0 + step < n_q ? a.l.rows[t0 + step].ncols : 0;
         for (int t = t0; t < n_q && alive; t += step) {
-            const int nt = __shfl_sync(0xffffffffu, (nx + 127) >> 7, 0);
+            const int nt = __shfl_sync(0xffffffffu, tiles(nx), 0);
             nx = nx2;
             if (t + 2 * step < n_q) nx2 = a.l.rows[t + 2 * step].ncols;
             if (nt == 0) continue;
@@ -634,7 +641,7 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
             if (st < HP) w[st] = wnext;
             if (t + step < n_q) wnext = st < H ? a.l.W[(int64_t)(t + step) * H + st] : 0.f;
             named_barrier(1 + set, 128);
-            const int nt = (ncols + 127) >> 7;
+            const int nt = tiles(ncols);
             if constexpr (!BWD) {
                 for (int i = (n & 1) == set ? 0 : 1; i < nt; i += 2) {   // the set's tiles
                     const int g = n + i;   // the CTA's tile number
@@ -645,7 +652,7 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
                     tmem_load<HP>(tS + set * 64 + lanes, v);
                     tc_fence_before();
                     mbar_arrive(&sfree[set]);
-                    const int j = i * 128 + lrow;
+                    const int j = (p + i * P) * 128 + lrow;
                     uint64_t acc = 0;   // even heads and odd heads
 #pragma unroll
                     for (int h = 0; h < HP; h += 4) {
@@ -657,8 +664,8 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
                     unpack_f32x2(acc, s0, s1);
                     if (j < k) a.l.scores[(int64_t)t * k + j] = j < ncols ? (s0 + s1) + 0.f : -CUDART_INF_F;
                 }
-                if (set == 0)   // places behind the last tile
-                    for (int j = nt * 128 + st; j < k; j += 128) a.l.scores[(int64_t)t * k + j] = -CUDART_INF_F;
+                if (set == 0 && p == 0)   // places behind the last tile
+                    for (int j = ((ncols + 127) & ~127) + st; j < k; j += 128) a.l.scores[(int64_t)t * k + j] = -CUDART_INF_F;
             } else {
                 constexpr int NC = HP / 2;     // heads (columns) of a set
                 const int grp = set >> 1, half = set & 1, c0 = half * NC;

@@ -351,13 +351,15 @@ dsa_status list_tc_launch(const ListArgs& l, int32_t t0, int32_t t1, const ListP
     using SH = ListShape<D, HP>;
     CUtensorMap mq;
     if (!make_tile_map(&mq, l.Q, int64_t(l.n_q) * l.H, D, l.H)) return DSA_ERR_CUDA;
-    const ListTcArgs a{l, std::min(8, int((kSmemMax - SH::bytes(0, MODE == kListGradRows)) / SH::KTILE)), t0, t1,
+    // few queries: several CTAs each, as many as fill the GPU once and find at least two tiles
+    const int splits = MODE == kListScores ? std::max(1, std::min(148 / (t1 - t0), (l.k + 255) / 256)) : 1;
+    const ListTcArgs a{l, std::min(8, int((kSmemMax - SH::bytes(0, MODE == kListGradRows)) / SH::KTILE)), t0, t1, splits,
                        p.part, p.bits, p.pre, p.off, p.base};
     const int smem = std::max<int>(SH::bytes(a.n_stages, MODE == kListGradRows), 120 * 1024);   // one CTA an SM
     dsa_status s = set_smem(list_tc_kernel<D, HP, MODE>, smem);
     if (s != DSA_OK) return s;
     DSA_LAUNCH(MODE ? kProfListDq : kProfListScores, st,
-               launch_pdl(true, list_tc_kernel<D, HP, MODE>, std::min(t1 - t0, 148), list_threads(MODE), smem, st, mq, a));
+               launch_pdl(true, list_tc_kernel<D, HP, MODE>, std::min((t1 - t0) * splits, 148), list_threads(MODE), smem, st, mq, a));
     return launched();
 }
 

@@ -402,6 +402,17 @@ def test_list_scores_long_lists_and_few_queries():
     check_lists(b, random_lists(g, b, 16384), randn(g, 3, 16384))
 
 
+@pytest.mark.parametrize("H,d,k", [(64, 128, 1000), (32, 64, 257), (16, 32, 4001), (4, 128, 129), (64, 64, 128)])
+def test_list_scores_few_queries_share_the_gpu(H, d, k):
+    """A few queries, whose tiles several CTAs take in turn: lists that end in any of them, empty ones, one place."""
+    b = workloads.ragged(H + k, [3, 1, 2], [5000, 40, 900], H=H, d=d, k=k, integer=False)
+    g = gen(k)
+    lists = random_lists(g, b, k)
+    lists[1] = -1
+    lists[2, 1:] = -1
+    check_lists(b, lists, randn(g, b.n_q, k))
+
+
 def test_list_scores_nothing_to_do():
     b = workloads.ragged(61, [0, 0], [30, 5], H=4, d=32, k=8, integer=False)
     lay, Q, K, W = on_gpu(b)
