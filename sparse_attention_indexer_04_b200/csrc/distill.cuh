@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(NT) distill_kernel(const __grid_constant__ Dis
     }
 }
 
-// One row at a time per CTA, rows NT * 4 * (NV - 1) < k <= NT * 4 * NV long, with the next row's places on
+// One row at a time per CTA, of at most NT * 4 * NV places, with the next row's places on
 // their way to shared memory while this one is worked on (a CTA per row holds so many registers that
 // it is alone on its SM, and its loads, sums and stores then follow one another: 78 us for
 // 1021 x 20011).  A thread copies the places that it reads itself, so it waits for its own copies alone;
@@ -274,7 +274,7 @@ template <typename TT, bool WEIGHTS, bool EDGE, int NV, int NT, int CTAS>
 __global__ void __launch_bounds__(NT, CTAS) distill_ring_kernel(const __grid_constant__ DistillArgs a)
 {
     extern __shared__ __align__(16) uint8_t dyn[];
-    __shared__ float4 red1[32], red2[32];
+    __shared__ float4 red1[NT / 32], red2[NT / 32];
     const int t = threadIdx.x;
     float4* ss = reinterpret_cast<float4*>(dyn);                                    // [NV][NT] scores
     int4* sl = reinterpret_cast<int4*>(ss + NV * NT);                               // [NV][NT] lists, if given

@@ -137,9 +137,18 @@ dsa_status distill_ring(const DistillArgs& a, cudaStream_t st)
 {
     const auto kern = distill_ring_kernel<TT, WEIGHTS, EDGE, NV, NT, CTAS>;
     const size_t smem = size_t(NV) * NT * (16 + 4 * sizeof(TT) + (a.list ? 16 : 0));
-    dsa_status s = set_smem(kern, smem);
+    // the limit counts lists either way: calls at the same time may set it to one value only
+    dsa_status s = set_smem(kern, std::min(size_t(NV) * NT * (32 + 4 * sizeof(TT)), size_t(200) * 1024));
     if (s != DSA_OK) return s;
-    DSA_LAUNCH(kProfDistill, st, kern<<<std::min(a.n, 148 * CTAS), NT, smem, st>>>(a));
+    // lists and fp32 teachers: three quarters of the CTAs and of the shared memory, since rows of 192 KB
+    // together leave the L1 too little for their loads and stores (9000 x 2000: 66 us, so 50; the other
+    // types' rows come to 128 or 160 KB: 38 and 46 us, and no faster with fewer)
+    const bool wide = CTAS > 1 && a.list && sizeof(TT) == 4;
+    const int ctas = wide ? CTAS * 3 / 4 : CTAS;
+    const int share = wide ? int(ctas * (smem + 2048) * 100 / (228 * 1024)) + 1 : (int)cudaSharedmemCarveoutDefault;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, share) != cudaSuccess)
+        return DSA_ERR_CUDA;
+    DSA_LAUNCH(kProfDistill, st, kern<<<std::min(a.n, 148 * ctas), NT, smem, st>>>(a));
     return launched();
 }
 
@@ -151,15 +160,17 @@ dsa_status distill_pick(const DistillArgs& a, cudaStream_t st)
     const int32_t k = EDGE ? a.k + 3 : a.k;   // columns from the boundary before the row
     if (k <= 128) return distill_launch<TT, WEIGHTS, VEC, EDGE, 32, 1 * U, 256>(a, st);
     if (k <= 512) return distill_launch<TT, WEIGHTS, VEC, EDGE, 32, 4 * U, 256>(a, st);
-    if (k <= 1024) return distill_launch<TT, WEIGHTS, VEC, EDGE, 64, 4 * U, 64>(a, st);
     // many rows: the next one read ahead, with as many CTAs an SM as hold rows of 64 KB together
-    // (9765 x 2048: 51.9 us without, 43.5 with, fp32); not for rows off the 16-byte boundaries, whose
-    // end vectors cost more there (9765 x 2049: 78 us without, 88 with)
+    // (18000 x 1000: 46.2 us without, 37.7 with, 9000 x 2000 47.7 and 38.2, 2250 x 8000 55.5 and 41.0, fp32);
+    // not for rows off the 16-byte boundaries, whose end vectors cost more there (9765 x 2049: 78 us
+    // without, 88 with)
     if constexpr (VEC == 4 && !EDGE) {
+        if (k > 512 && k <= 1024 && a.n > 148 * 16) return distill_ring<TT, WEIGHTS, EDGE, 4, 64, 16>(a, st);
         if (k > 1024 && k <= 2048 && a.n > 148 * 8) return distill_ring<TT, WEIGHTS, EDGE, 4, 128, 8>(a, st);
         if (k > 2048 && k <= 4096 && a.n > 148 * 4) return distill_ring<TT, WEIGHTS, EDGE, 4, 256, 4>(a, st);
         if (k > 4096 && k <= 8192 && a.n > 148 * 2) return distill_ring<TT, WEIGHTS, EDGE, 4, 512, 2>(a, st);
     }
+    if (k <= 1024) return distill_launch<TT, WEIGHTS, VEC, EDGE, 64, 4 * U, 64>(a, st);
     if (k <= 2048) return distill_launch<TT, WEIGHTS, VEC, EDGE, 128, 4 * U, 128>(a, st);
     if (k <= 4096) return distill_launch<TT, WEIGHTS, VEC, EDGE, 256, 4 * U, 256>(a, st);
     if (k <= 8192) return distill_launch<TT, WEIGHTS, VEC, EDGE, 512, 4 * U, 512>(a, st);

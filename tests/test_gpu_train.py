@@ -184,6 +184,25 @@ def test_distill(k, tt, weights, lists):
         ref.check(ds, wd, ed, F32, f"ds n={n}")
 
 
+@pytest.mark.parametrize("n,k", [(2500, 516), (2380, 1024), (4750, 613), (1250, 1028), (1190, 2048), (600, 2900),
+                                 (299, 6000), (300, 8192)])
+@pytest.mark.parametrize("tt,weights,lists", [(F32, False, True), (BF, False, False), (BF, True, True)])
+def test_distill_many_rows(n, k, tt, weights, lists):
+    """More rows than fit the GPU at once: the CTAs take several each, and read ahead where rows are aligned;
+    the gradient over its scores gives the same."""
+    g = gen(n + k)
+    s, t, l = distill_case(g, n, k, tt, weights, lists)
+    gr = randn(g, n)
+    kind = dsa.TEACHER_WEIGHTS if weights else dsa.TEACHER_LOGITS
+    sd, td, ld = s.to(DEV), t.to(DEV), None if l is None else l.to(DEV)
+    loss, ds = dsa.distill_topk(sd, td, lists=ld, kind=kind, temperature=0.5, grad_loss=gr.to(DEV))
+    (wl, wd), (el, ed) = ref.distill(s, t, l, weights, 0.5, gr)
+    ref.check(loss, wl, el, F32, "loss")
+    ref.check(ds, wd, ed, F32, "ds")
+    loss2, ds2 = dsa.distill_topk(sd, td, lists=ld, kind=kind, temperature=0.5, grad_loss=gr.to(DEV), dscores=sd)
+    assert ds2.data_ptr() == sd.data_ptr() and torch.equal(loss, loss2) and torch.equal(ds, ds2)
+
+
 def test_distill_in_place_alone_and_same_bits():
     g = gen(11)
     for k in (96, 2048, 20000):
