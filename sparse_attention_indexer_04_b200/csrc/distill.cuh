@@ -356,9 +356,11 @@ __global__ void __launch_bounds__(NT, CTAS) distill_ring_kernel(const __grid_con
     }
 }
 
-// Rows of any length: one CTA per row, two sweeps.  In the first a thread keeps running maxima and
-// sums, rescaled when a batch of places raises a maximum; the CTA then brings its threads' sums to the
-// row's maxima and joins them; the second writes the gradient.
+// Rows of any length: one CTA per row, two sweeps.  In the first a thread keeps running maxima and the
+// sums z and y, rescaled when a batch of places raises a maximum (by 0 where that is out of reach); the
+// CTA then brings its threads' sums to the row's maxima and joins them.  The second writes the gradient
+// and adds up the cross sum: it needs the row's maxima, since a running one would carry terms of places
+// whose weight the row's maximum makes zero (f = 0 times an infinite rescaling is no number).
 template <typename TT, bool WEIGHTS, int NT>
 __global__ void __launch_bounds__(NT) distill_long_kernel(const __grid_constant__ DistillArgs a)
 {
@@ -381,20 +383,15 @@ __global__ void __launch_bounds__(NT) distill_long_kernel(const __grid_constant_
         for (int i = 0; i < BATCH; ++i)
             if (s[i] == -CUDART_INF_F) v[i] = WEIGHTS ? 0.f : -CUDART_INF_F;
     };
-    // to maxima m and n: exponents shift by (m - ms) and, for logits, (n - mt); with nothing summed yet the
-    // old maximum is -inf and the sums are zero whatever they are scaled by
-    float ms = -CUDART_INF_F, mt = -CUDART_INF_F, z = 0.f, y = 0.f, x = 0.f;
+    // to maxima m and n; nothing is summed while one is -inf
+    float ms = -CUDART_INF_F, mt = -CUDART_INF_F, z = 0.f, y = 0.f;
     auto raise = [&](float m, float n) {
         if (m > ms) {
-            const float up = ms == -CUDART_INF_F ? 0.f : (m - ms) * a.scale;
-            z *= distill_exp2(-up);
-            x = fmaf(y, up, x);
+            if (ms != -CUDART_INF_F) z *= distill_exp2((ms - m) * a.scale);
             ms = m;
         }
         if (!WEIGHTS && n > mt) {
-            const float up = mt == -CUDART_INF_F ? 0.f : (n - mt) * a.scale, f = distill_exp2(-up);
-            x = (x - y * up) * f;
-            y *= f;
+            if (mt != -CUDART_INF_F) y *= distill_exp2((mt - n) * a.scale);
             mt = n;
         }
     };
@@ -410,36 +407,39 @@ __global__ void __launch_bounds__(NT) distill_long_kernel(const __grid_constant_
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
             if (s[i] == -CUDART_INF_F) continue;
-            const float d = (s[i] - ms) * a.scale;
-            z += distill_exp2(d);
-            float lg, w = 0.f;
-            if (WEIGHTS || mt != -CUDART_INF_F) w = distill_weight<WEIGHTS>(v[i], mt, a, lg);
-            y += w;
-            if (w != 0.f) x = fmaf(w, lg - d, x);
+            z += distill_exp2((s[i] - ms) * a.scale);
+            float lg;
+            if (WEIGHTS || mt != -CUDART_INF_F) y += distill_weight<WEIGHTS>(v[i], mt, a, lg);
         }
     }
-    float m = ms, n = mt;
+    float m = ms, n = mt, x = 0.f;
     distill_max2<NT>(m, n, red1);
     raise(m, n);
     distill_sum3<NT>(z, y, x, red2);
-    const DistillRow r = distill_row(z, y, x, a.g ? a.g[row] : 1.f, a);
-    if (threadIdx.x == 0 && a.loss) a.loss[row] = r.loss;
-    if (!a.ds) return;
-    float* dp = a.ds + (int64_t)row * a.ld_ds;
+    const float g = a.g ? a.g[row] : 1.f;
+    DistillRow r = distill_row(z, y, x, g, a);
+    float* dp = a.ds ? a.ds + (int64_t)row * a.ld_ds : nullptr;
     for (int64_t c0 = threadIdx.x; c0 < a.k; c0 += (int64_t)BATCH * NT) {
         read(c0);
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
             const int64_t c = c0 + (int64_t)i * NT;
             if (c >= a.k) continue;
-            float lg, out = 0.f;
+            float e = 0.f, w = 0.f;
             if (s[i] != -CUDART_INF_F) {
-                out = distill_exp2((s[i] - ms) * a.scale) * r.cs;
-                if (WEIGHTS || mt != -CUDART_INF_F) out -= distill_weight<WEIGHTS>(v[i], mt, a, lg) * r.ct;
+                const float d = (s[i] - ms) * a.scale;
+                e = distill_exp2(d);
+                float lg;
+                if (WEIGHTS || mt != -CUDART_INF_F) w = distill_weight<WEIGHTS>(v[i], mt, a, lg);
+                if (w != 0.f) x = fmaf(w, lg - d, x);
             }
-            dp[c] = out;
+            if (dp) dp[c] = distill_grad(e, w, r);
         }
     }
+    if (!a.loss) return;
+    float unused1 = 0.f, unused2 = 0.f;
+    distill_sum3<NT>(x, unused1, unused2, red1);
+    if (threadIdx.x == 0) a.loss[row] = distill_row(z, y, x, g, a).loss;
 }
 
 }  // namespace dsa

@@ -1,0 +1,159 @@
+"""The distillation loss where its arithmetic or its indices can go wrong: rows of every kernel form, long ones among
+them, with masks of the type's lowest value."""
+import math
+
+import pytest
+import torch
+
+import sparse_attention_indexer_04_b200 as dsa
+from train_ref import U, check
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+LOW = torch.finfo(F32).min
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def reference(s, t, lists, weights, tau, g):
+    """((loss, ds), bounds) in 64 bits, rows together.
+
+    An exponential's argument has three roundings of a value of magnitude |a| (3 U |a|), the exponential 4 U more; one
+    whose |a| is above 104 is zero in fp32, or an error of 2^-126 of the row's largest.  A sum is taken by threads that
+    hold k/512 terms at most and joined in 64 steps; where a running sum is rescaled, each batch of 8 terms may add a
+    factor (5 U) whose argument is again at most 104, or that is zero.  So q and p are off by
+    rel = 2 (3 A + k/512 + 5 k/4096 + 4 A + 116) U of themselves, A = min(max |a|, 104), twice for numerator and
+    denominator together; the factors 2^-126 come to less than 2^-100.  The loss adds the cross terms' own roundings."""
+    s, t = s.double(), t.double()
+    n, k = s.shape
+    live = s > -math.inf
+    if lists is not None:
+        live &= lists >= 0
+    gr = torch.ones(n).double() if g is None else g.double()
+    ninf = torch.full_like(s, -math.inf)
+    a = torch.where(live, s, ninf) / tau
+    a = a - a.amax(1, keepdim=True)
+    zero = torch.zeros_like(s)
+    if weights:
+        v = torch.where(live, t, zero)
+        p, logp = v / v.sum(1, keepdim=True), torch.log(v) - torch.log(v.sum(1, keepdim=True))
+    else:
+        v = torch.where(live, t, ninf) / tau
+        v = v - v.amax(1, keepdim=True)
+        p, logp = v.softmax(1), v.log_softmax(1)
+    q, logq = a.softmax(1), a.log_softmax(1)
+    ok = live.any(1) & ~p.isnan().any(1) & (p.sum(1) > 0)
+    on = live & (p > 0) & ok[:, None]
+    cross = torch.where(on, p * (logp - logq), zero)
+    loss = torch.where(ok, cross.sum(1), torch.zeros(n).double())
+    scale = (gr / tau)[:, None]
+    ds = torch.where(live & ok[:, None], scale * (q - p), zero)
+    size = torch.where(live & (a.abs() < 104), a.abs(), zero).amax(1)
+    rel = 2 * (7 * size + k / 512 + 5 * k / 4096 + 116) * U
+    e_ds = torch.where(live & ok[:, None], scale.abs() * ((q + p) * rel[:, None] + 2.0 ** -100), zero)
+    mag = torch.where(on, p * (logp.abs() + logq.abs()), zero).sum(1)
+    e_loss = torch.where(ok, rel * mag + 2 * rel + 2.0 ** -100, torch.zeros(n).double())
+    return (loss, ds), (e_loss, e_ds)
+
+
+def values(g, n, k, tt, weights, lists):
+    """Scores, teacher and lists with dropped places; whatever stands in those does not count."""
+    s, t = torch.randn(n, k, generator=g) * 2, torch.randn(n, k, generator=g) * 2
+    if weights:
+        t = t.exp()
+    drop = torch.rand(n, k, generator=g) < 0.3
+    drop[:, -1] = False
+    l = None
+    if lists:
+        l = torch.randint(0, 9, (n, k), generator=g, dtype=torch.int32)
+        l[drop] = -1
+        s[drop] = math.nan
+    else:
+        s[drop] = -math.inf
+    t = t.to(tt)
+    t[drop] = math.nan
+    return s, t, l
+
+
+def run(s, t, l, weights, tau, gr=None, off=0, pad=0, into=None):
+    """distill_topk on the rows as slices of wider matrices; into: "scores" writes the gradient over them."""
+    n, k = s.shape
+
+    def wide(x, fill):
+        big = torch.full((n, k + off + pad), fill, dtype=x.dtype, device=DEV)
+        big[:, off:off + k] = x.to(DEV)
+        return big, big[:, off:off + k]
+    _, ss = wide(s, 7)
+    _, ts = wide(t, 7)
+    ls = None if l is None else wide(l, 5)[1]
+    big, ds = wide(torch.zeros(n, k), math.nan)
+    if into == "scores":
+        ds = ss
+    loss, ds = dsa.distill_topk(ss, ts, lists=ls, kind=int(weights), temperature=tau,
+                                grad_loss=None if gr is None else gr.to(DEV), dscores=ds)
+    torch.cuda.synchronize()
+    rest = torch.cat([big[:, :off], big[:, off + k:]], 1)
+    assert bool(torch.isnan(rest).all()), "written outside the rows"
+    return loss, ds
+
+
+KINDS = [(F32, False, True), (BF, False, False), (BF, True, True), (F32, True, False)]
+
+
+@pytest.mark.parametrize("k", [20481, 20484, 40003])
+@pytest.mark.parametrize("tt,weights,lists", KINDS)
+def test_rows_of_any_length(k, tt, weights, lists):
+    """Rows longer than a CTA's registers hold."""
+    g = gen(k)
+    for n, off, pad, tau in ((3, 0, 0, 1.0), (2, 1, 3, 0.5)):
+        s, t, l = values(g, n, k, tt, weights, lists)
+        gr = torch.randn(n, generator=g)
+        want, bound = reference(s, t, l, weights, tau, gr)
+        for into in (None, "scores"):
+            got = run(s, t, l, weights, tau, gr, off, pad, into)
+            for a, w, e, name in zip(got, want, bound, ("loss", "ds")):
+                check(a, w, e, F32, f"{name} n={n}")
+
+
+@pytest.mark.parametrize("k", [100, 513, 2048, 9001, 20000, 40000])
+@pytest.mark.parametrize("tt", [F32, BF])
+def test_masks_of_the_lowest_value(k, tt):
+    """Teacher logits, or teacher logits and scores, masked with the type's lowest value: at the row's start (past a
+    long row's first batches), in all places of some threads, and everywhere but one."""
+    g = gen(k + 1)
+    s, t, _ = values(g, 6, k, tt, False, False)
+    s.nan_to_num_(neginf=0.0)
+    t.nan_to_num_(0.0)
+    first = max(1, min(8192, k - 1))
+    t[0, :first] = torch.finfo(tt).min
+    t[1, :first] = torch.finfo(tt).min
+    s[1, :first] = LOW
+    t[2, :-1] = torch.finfo(tt).min
+    s[2, :-1] = LOW
+    t[3, 0::2] = torch.finfo(tt).min
+    s[3, 0::2] = LOW
+    t[4] = torch.finfo(tt).min        # all alike: uniform
+    t[5, -first:] = torch.finfo(tt).min
+    s[5, -first:] = LOW
+    want, bound = reference(s, t, None, False, 1.0, None)
+    for a, w, e, name in zip(run(s, t, None, False, 1.0), want, bound, ("loss", "ds")):
+        check(a, w, e, F32, name)
+
+
+@pytest.mark.parametrize("k", [100, 513, 2048, 9001, 20000, 40000])
+def test_weights_over_scores_of_the_lowest_value(k):
+    """Scores masked with the lowest value where the teacher's weights are zero."""
+    g = gen(k + 2)
+    s, t, _ = values(g, 3, k, F32, True, False)
+    s.nan_to_num_(neginf=0.0)
+    t.nan_to_num_(1.0)
+    first = max(1, min(8192, k - 1))
+    t[0, :first], s[0, :first] = 0.0, LOW
+    t[1, 0::2], s[1, 0::2] = 0.0, LOW
+    t[2, :-1], s[2, :-1] = 0.0, LOW
+    want, bound = reference(s, t, None, True, 1.0, None)
+    for a, w, e, name in zip(run(s, t, None, True, 1.0), want, bound, ("loss", "ds")):
+        check(a, w, e, F32, name)
