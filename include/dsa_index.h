@@ -318,6 +318,8 @@ dsa_status dsa_layer_norm_backward(int64_t n, int32_t d, const void* dy, int32_t
  * grad_loss [n] or NULL (ones); loss [n] or NULL; dscores or NULL, which may
  * be scores' own memory with the same stride.  A row with no counted place,
  * or none that the teacher gives weight, has loss 0 and gradient 0.
+ * 2^-64 <= temperature <= 2^64 (else DSA_ERR_INVALID_ARG).  Scores and logits may be
+ * masked with their type's lowest value; a loss beyond fp32's range is inf.
  */
 dsa_status dsa_distill_topk(int32_t n, int32_t k, const float* scores, int64_t ld_scores, const int32_t* lists,
                             int64_t ld_lists, const void* teacher, int32_t teacher_type, int64_t ld_teacher,

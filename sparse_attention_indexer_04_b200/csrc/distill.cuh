@@ -9,6 +9,9 @@
 // logarithm c_j (c_j = (t_j - max t) / tau, f = e^c; or f = t, c = log t) and y = sum f:
 //   loss = (sum f (c - a)) / y + log z - log y,
 // so two joint reductions over the row (the maxima, then z, y and the cross sum) give everything.
+// Differences from the maxima are taken in units of 2^24 (exact, one fma each) and the cross sum is kept
+// in those: a score masked with the type's lowest value is 3.4e38 below the maximum, which neither the
+// factor log2(e) / tau nor a sum over 2^24 such places may carry past fp32.
 // Bound by memory: a row is read once into registers and its gradient written once.  Exponentials
 // are base 2, one multiply and one instruction each (with expf and logf the arithmetic took as long
 // as the memory: 61.6 us for 8192 x 2048).  Rows longer than the registers of a CTA hold
@@ -38,7 +41,8 @@ struct DistillArgs {
     int64_t ld_ds;
     int32_t n, k;
     float inv_tau;
-    float scale;           // log2(e) / tau: exponents are taken to base 2
+    float scale;           // 2^24 log2(e) / tau: exponents are taken to base 2, of differences in units of 2^24
+    float unit_log2;       // tau ln 2 / 2^24: a base-2 logarithm in those units
     int32_t off0, off_step; // VEC 4: row r starts (off0 + r * off_step) % 4 places behind a 4-place boundary
 };
 
@@ -138,16 +142,21 @@ __device__ __forceinline__ float distill_log2(float x)
     return y;
 }
 
-// The teacher's unnormalised weight of a place and its base-2 logarithm c (a logit of -inf: 0 and -inf).
+constexpr float kDistillUnit = 16777216.f;   // 2^24
+
+// x - max in units of 2^24; unit_max = -max / 2^24.
+__device__ __forceinline__ float distill_below(float x, float unit_max) { return fmaf(x, 1.f / kDistillUnit, unit_max); }
+
+// The teacher's unnormalised weight of a place and its logarithm c, times tau / 2^24 (a logit of -inf: 0 and -inf).
 template <bool WEIGHTS>
-__device__ __forceinline__ float distill_weight(float t, float mt, const DistillArgs& a, float& c)
+__device__ __forceinline__ float distill_weight(float t, float unit_mt, const DistillArgs& a, float& c)
 {
     if constexpr (WEIGHTS) {
-        c = distill_log2(t);
+        c = distill_log2(t) * a.unit_log2;
         return t;
     } else {
-        c = (t - mt) * a.scale;
-        return distill_exp2(c);
+        c = distill_below(t, unit_mt);
+        return distill_exp2(c * a.scale);
     }
 }
 
@@ -165,18 +174,19 @@ __device__ __forceinline__ void distill_maxima(const float* s, float* f, float& 
 }
 
 // From the row's maxima (0 in place of -inf, so that -inf gives weight 0): s becomes e^a, f the teacher's
-// weight; their sums and the cross sum grow.
+// weight; their sums and the cross sum grow (that in units of 2^24 / tau).
 template <bool WEIGHTS, int N>
 __device__ __forceinline__ void distill_sums(float* s, float* f, float ms, float mt, const DistillArgs& a, float& z,
                                              float& y, float& x)
 {
+    const float um = -ms / kDistillUnit, ut = -mt / kDistillUnit;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-        const float d = (s[e] - ms) * a.scale;
-        s[e] = distill_exp2(d);
+        const float d = distill_below(s[e], um);
+        s[e] = distill_exp2(d * a.scale);
         z += s[e];
         float c;
-        f[e] = distill_weight<WEIGHTS>(f[e], mt, a, c);
+        f[e] = distill_weight<WEIGHTS>(f[e], ut, a, c);
         y += f[e];
         if (f[e] != 0.f) x = fmaf(f[e], c - d, x);
     }
@@ -192,7 +202,7 @@ __device__ __forceinline__ DistillRow distill_row(float z, float y, float x, flo
 {
     DistillRow r{0.f, 0.f, 0.f, true};
     if (y == 0.f || z == 0.f) return r;   // no counted place, or none that the teacher weighs: nothing to learn
-    r.loss = x / y * 0.69314718055994531f + (logf(z) - logf(y));
+    r.loss = x / y * kDistillUnit * a.inv_tau + (logf(z) - logf(y));
     r.cs = g * a.inv_tau / z;
     r.ct = g * a.inv_tau / y;
     r.sound = isfinite(r.cs) && isfinite(r.ct);
@@ -387,11 +397,11 @@ __global__ void __launch_bounds__(NT) distill_long_kernel(const __grid_constant_
     float ms = -CUDART_INF_F, mt = -CUDART_INF_F, z = 0.f, y = 0.f;
     auto raise = [&](float m, float n) {
         if (m > ms) {
-            if (ms != -CUDART_INF_F) z *= distill_exp2((ms - m) * a.scale);
+            if (ms != -CUDART_INF_F) z *= distill_exp2(distill_below(ms, -m / kDistillUnit) * a.scale);
             ms = m;
         }
         if (!WEIGHTS && n > mt) {
-            if (mt != -CUDART_INF_F) y *= distill_exp2((mt - n) * a.scale);
+            if (mt != -CUDART_INF_F) y *= distill_exp2(distill_below(mt, -n / kDistillUnit) * a.scale);
             mt = n;
         }
     };
@@ -407,9 +417,9 @@ __global__ void __launch_bounds__(NT) distill_long_kernel(const __grid_constant_
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
             if (s[i] == -CUDART_INF_F) continue;
-            z += distill_exp2((s[i] - ms) * a.scale);
-            float lg;
-            if (WEIGHTS || mt != -CUDART_INF_F) y += distill_weight<WEIGHTS>(v[i], mt, a, lg);
+            z += distill_exp2(distill_below(s[i], -ms / kDistillUnit) * a.scale);
+            float c;
+            if (WEIGHTS || mt != -CUDART_INF_F) y += distill_weight<WEIGHTS>(v[i], -mt / kDistillUnit, a, c);
         }
     }
     float m = ms, n = mt, x = 0.f;
@@ -427,10 +437,10 @@ __global__ void __launch_bounds__(NT) distill_long_kernel(const __grid_constant_
             if (c >= a.k) continue;
             float e = 0.f, w = 0.f;
             if (s[i] != -CUDART_INF_F) {
-                const float d = (s[i] - ms) * a.scale;
-                e = distill_exp2(d);
+                const float d = distill_below(s[i], -ms / kDistillUnit);
+                e = distill_exp2(d * a.scale);
                 float lg;
-                if (WEIGHTS || mt != -CUDART_INF_F) w = distill_weight<WEIGHTS>(v[i], mt, a, lg);
+                if (WEIGHTS || mt != -CUDART_INF_F) w = distill_weight<WEIGHTS>(v[i], -mt / kDistillUnit, a, lg);
                 if (w != 0.f) x = fmaf(w, lg - d, x);
             }
             if (dp) dp[c] = distill_grad(e, w, r);

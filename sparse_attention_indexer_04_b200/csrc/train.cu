@@ -124,6 +124,9 @@ size_t norm_ws_bytes(int64_t n, int32_t d)
 
 // ------------------------------------------------------------ distillation
 
+// 2^-64 and 2^64: factors of it, and differences of scores of its size in units of 2^24, stay normal numbers.
+constexpr float kMinTemperature = 5.42101086e-20f, kMaxTemperature = 1.84467441e19f;
+
 template <typename TT, bool WEIGHTS, int VEC, bool EDGE, int T, int NV, int NT>
 dsa_status distill_launch(const DistillArgs& a, cudaStream_t st)
 {
@@ -529,9 +532,7 @@ dsa_status dsa_distill_topk(int32_t n, int32_t k, const float* scores, int64_t l
                             int32_t teacher_kind, float temperature, const float* grad_loss, float* loss,
                             float* dscores, int64_t ld_dscores, void* stream)
 {
-    if (n < 0 || k < 1 || !(temperature > 0.f) || !std::isfinite(temperature) ||
-        !std::isfinite(1.f / temperature))
-        return DSA_ERR_INVALID_ARG;
+    if (n < 0 || k < 1 || !(temperature >= kMinTemperature && temperature <= kMaxTemperature)) return DSA_ERR_INVALID_ARG;
     if (teacher_kind != DSA_TEACHER_LOGITS && teacher_kind != DSA_TEACHER_WEIGHTS) return DSA_ERR_INVALID_ARG;
     dsa_status s;
     if ((s = check_rows(scores, DSA_FP32, ld_scores, n, k)) != DSA_OK) return s;
@@ -544,7 +545,8 @@ dsa_status dsa_distill_topk(int32_t n, int32_t k, const float* scores, int64_t l
     a.s = scores; a.ld_s = ld_scores; a.list = lists; a.ld_list = ld_lists; a.t = teacher; a.ld_t = ld_teacher;
     a.g = grad_loss; a.loss = loss; a.ds = dscores; a.ld_ds = ld_dscores; a.n = n; a.k = k;
     a.inv_tau = 1.f / temperature;
-    a.scale = (float)(1.4426950408889634 / (double)temperature);
+    a.scale = (float)(1.4426950408889634 * kDistillUnit / (double)temperature);
+    a.unit_log2 = (float)(0.69314718055994531 / kDistillUnit * (double)temperature);
     // four places a load where the arrays' rows lie alike against 4-place boundaries
     const auto place = [](const void* p, int64_t size) { return int32_t(reinterpret_cast<uintptr_t>(p) / size % 4); };
     a.off0 = place(scores, 4);

@@ -157,3 +157,33 @@ def test_weights_over_scores_of_the_lowest_value(k):
     want, bound = reference(s, t, None, True, 1.0, None)
     for a, w, e, name in zip(run(s, t, None, True, 1.0), want, bound, ("loss", "ds")):
         check(a, w, e, F32, name)
+
+
+@pytest.mark.parametrize("k", [100, 513, 2048, 9001, 20000, 40000])
+@pytest.mark.parametrize("tt,weights", [(F32, False), (BF, False), (F32, True), (BF, True)])
+def test_scores_of_the_lowest_value_that_the_teacher_weighs(k, tt, weights):
+    """The loss is large (up to 1e38) and finite: one such place, half of the places, a few of little weight."""
+    g = gen(k + 3)
+    s, t, _ = values(g, 4, k, tt, weights, False)
+    s.nan_to_num_(neginf=0.0)
+    t.nan_to_num_(0.5)
+    s[0, 3] = LOW
+    s[1, 0::2] = LOW
+    s[2, :3] = LOW
+    t[2, :3] = 2.0 ** -100 if weights else -60.0
+    s[3, -40:] = LOW
+    for tau in (1.0, 2.0):
+        want, bound = reference(s, t, None, weights, tau, None)
+        assert bool((want[0] > 100).all()) and bool((want[0] < 3e38).all())
+        for a, w, e, name in zip(run(s, t, None, weights, tau), want, bound, ("loss", "ds")):
+            check(a, w, e, F32, f"{name} tau={tau}")
+
+
+def test_temperatures_the_arithmetic_does_not_hold_are_refused():
+    x = torch.zeros(2, 8, device=DEV)
+    for tau in (3e-39, 1e-30, 1e30, 3e38):
+        with pytest.raises(dsa.DsaError):
+            dsa.distill_topk(x, x, temperature=tau)
+    for tau in (1e-18, 1e18):
+        loss, ds = dsa.distill_topk(x, x, temperature=tau)
+        assert not loss.any() and not ds.any()
