@@ -312,7 +312,7 @@ dsa_status dsa_layer_norm_backward(int64_t n, int32_t d, const void* dy, int32_t
  * count (NaN, infinities) has no effect.  Over the counted places
  *     q = softmax(scores / temperature),
  *     p = softmax(teacher / temperature)     (DSA_TEACHER_LOGITS; -inf: p = 0)
- *       = teacher / sum(teacher)             (DSA_TEACHER_WEIGHTS; >= 0),
+ *       = teacher / sum(teacher)             (DSA_TEACHER_WEIGHTS; >= 0, of any scale),
  *     loss[r] = sum p (log p - log q),
  *     dscores = grad_loss[r] / temperature * (q - p), 0 in places that do not count.
  * grad_loss [n] or NULL (ones); loss [n] or NULL; dscores or NULL, which may

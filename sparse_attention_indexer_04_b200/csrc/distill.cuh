@@ -6,12 +6,13 @@
 //   q = softmax(s / tau);  p = softmax(t / tau) (logits) or t / sum t (weights);
 //   loss = sum p (log p - log q);  ds_j = (g / tau) (q_j - p_j), 0 outside C.
 // With a_j = (s_j - max s) / tau, z = sum e^a, and the teacher's unnormalised weights f_j with
-// logarithm c_j (c_j = (t_j - max t) / tau, f = e^c; or f = t, c = log t) and y = sum f:
+// logarithm c_j (c_j = (t_j - max t) / tau, f = e^c; or f = t times the power of two that brings
+// max t to 1 .. 2, c = log f: weights and their sum may lie below and above fp32's normal range) and y = sum f:
 //   loss = (sum f (c - a)) / y + log z - log y,
 // so two joint reductions over the row (the maxima, then z, y and the cross sum) give everything.
 // Differences from the maxima are taken in units of 2^24 (exact, one fma each) and the cross sum is kept
 // in those: a score masked with the type's lowest value is 3.4e38 below the maximum, which neither the
-// factor log2(e) / tau nor a sum over 2^24 such places may carry past fp32.
+// factor log2(e) / tau nor a sum over millions of such places may carry past fp32.
 // Bound by memory: a row is read once into registers and its gradient written once.  Exponentials
 // are base 2, one multiply and one instruction each (with expf and logf the arithmetic took as long
 // as the memory: 61.6 us for 8192 x 2048).  Rows longer than the registers of a CTA hold
@@ -142,20 +143,32 @@ __device__ __forceinline__ float distill_log2(float x)
     return y;
 }
 
+// What brings the largest weight m to 1 .. 2 (up to 4 from 2^127 on; a subnormal one to 2^-23 or more): a power of two.
+__device__ __forceinline__ float distill_factor(float m)
+{
+    const int e = (__float_as_uint(m) >> 23) & 255;
+    return __uint_as_float((uint32_t)max(254 - max(e, 1), 1) << 23);
+}
+
 constexpr float kDistillUnit = 16777216.f;   // 2^24
 
 // x - max in units of 2^24; unit_max = -max / 2^24.
 __device__ __forceinline__ float distill_below(float x, float unit_max) { return fmaf(x, 1.f / kDistillUnit, unit_max); }
 
+// What distill_weight takes of the row's largest teacher value.
+template <bool WEIGHTS>
+__device__ __forceinline__ float distill_teacher(float mt) { return WEIGHTS ? distill_factor(mt) : -mt / kDistillUnit; }
+
 // The teacher's unnormalised weight of a place and its logarithm c, times tau / 2^24 (a logit of -inf: 0 and -inf).
 template <bool WEIGHTS>
-__device__ __forceinline__ float distill_weight(float t, float unit_mt, const DistillArgs& a, float& c)
+__device__ __forceinline__ float distill_weight(float t, float teacher, const DistillArgs& a, float& c)
 {
     if constexpr (WEIGHTS) {
-        c = distill_log2(t) * a.unit_log2;
-        return t;
+        const float f = t * teacher;
+        c = distill_log2(f) * a.unit_log2;
+        return f;
     } else {
-        c = distill_below(t, unit_mt);
+        c = distill_below(t, teacher);
         return distill_exp2(c * a.scale);
     }
 }
@@ -169,7 +182,7 @@ __device__ __forceinline__ void distill_maxima(const float* s, float* f, float& 
     for (int e = 0; e < N; ++e) {
         if (s[e] == -CUDART_INF_F) f[e] = WEIGHTS ? 0.f : -CUDART_INF_F;
         ms = fmaxf(ms, s[e]);
-        if (!WEIGHTS) mt = fmaxf(mt, f[e]);
+        mt = fmaxf(mt, f[e]);
     }
 }
 
@@ -179,7 +192,7 @@ template <bool WEIGHTS, int N>
 __device__ __forceinline__ void distill_sums(float* s, float* f, float ms, float mt, const DistillArgs& a, float& z,
                                              float& y, float& x)
 {
-    const float um = -ms / kDistillUnit, ut = -mt / kDistillUnit;
+    const float um = -ms / kDistillUnit, ut = distill_teacher<WEIGHTS>(mt);
 #pragma unroll
     for (int e = 0; e < N; ++e) {
         const float d = distill_below(s[e], um);
@@ -407,8 +420,8 @@ __global__ void __launch_bounds__(NT) distill_long_kernel(const __grid_constant_
         }
         ask(next);
     };
-    // -max in units of 2^24, 0 for a maximum of -inf (so that -inf gives weight 0)
-    auto below = [](float m) { return m == -CUDART_INF_F ? 0.f : -m / kDistillUnit; };
+    // maxima with 0 in place of -inf (so that -inf gives weight 0)
+    auto finite = [](float m) { return m == -CUDART_INF_F ? 0.f : m; };
     // to maxima m and n; nothing is summed while one is -inf
     float ms = -CUDART_INF_F, mt = -CUDART_INF_F, z = 0.f, y = 0.f;
     auto raise = [&](float m, float n) {
@@ -416,8 +429,10 @@ __global__ void __launch_bounds__(NT) distill_long_kernel(const __grid_constant_
             if (ms != -CUDART_INF_F) z *= distill_exp2(distill_below(ms, -m / kDistillUnit) * a.scale);
             ms = m;
         }
-        if (!WEIGHTS && n > mt) {
-            if (mt != -CUDART_INF_F) y *= distill_exp2(distill_below(mt, -n / kDistillUnit) * a.scale);
+        if (n > mt) {
+            if (mt != -CUDART_INF_F)
+                y *= WEIGHTS ? distill_factor(n) / distill_factor(mt)
+                             : distill_exp2(distill_below(mt, -n / kDistillUnit) * a.scale);
             mt = n;
         }
     };
@@ -431,7 +446,7 @@ __global__ void __launch_bounds__(NT) distill_long_kernel(const __grid_constant_
             n = fmaxf(n, v[i]);
         }
         raise(m, n);
-        const float um = below(ms), ut = below(mt);
+        const float um = -finite(ms) / kDistillUnit, ut = distill_teacher<WEIGHTS>(finite(mt));
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
             z += distill_exp2(distill_below(s[i], um) * a.scale);
@@ -445,7 +460,7 @@ __global__ void __launch_bounds__(NT) distill_long_kernel(const __grid_constant_
     distill_sum3<NT>(z, y, x, red2);
     const float g = a.g ? a.g[row] : 1.f;
     DistillRow r = distill_row(z, y, x, g, a);
-    const float um = below(ms), ut = below(mt);
+    const float um = -finite(ms) / kDistillUnit, ut = distill_teacher<WEIGHTS>(finite(mt));
     float* dp = a.ds ? a.ds + (int64_t)row * a.ld_ds : nullptr;
     ask(threadIdx.x);
     for (int64_t c0 = threadIdx.x; c0 < a.k; c0 += (int64_t)BATCH * NT) {

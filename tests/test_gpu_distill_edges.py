@@ -187,3 +187,28 @@ def test_temperatures_the_arithmetic_does_not_hold_are_refused():
     for tau in (1e-18, 1e18):
         loss, ds = dsa.distill_topk(x, x, temperature=tau)
         assert not loss.any() and not ds.any()
+
+
+@pytest.mark.parametrize("k", [5, 300, 2048, 9001, 20000, 40000])
+@pytest.mark.parametrize("tt", [F32, BF])
+def test_weights_of_any_scale(k, tt):
+    """Weights whose sum lies below the normal range of fp32, at its lower end, above its range, and rows whose weights
+    span it."""
+    g = gen(k + 4)
+    scales = [-149 if tt == F32 else -133, -140 if tt == F32 else -130, -126, -100, 0, 100, 119]
+    s = torch.randn(len(scales) + 2, k, generator=g) * 2
+    m = torch.randint(0, 200, s.shape, generator=g).double()
+    m[:, -1] = 200.0
+    t = torch.zeros(s.shape, dtype=torch.float64)
+    for r, e in enumerate(scales):
+        t[r] = m[r] * 2.0 ** e
+    span = torch.randint(-120, 120, (k,), generator=g).double()
+    t[-2] = 2.0 ** span
+    t[-1] = 2.0 ** span.sort().values
+    t = t.to(tt)
+    assert bool(torch.isfinite(t).all()) and bool((t.double().sum(1) > 0).all())
+    gr = torch.randn(s.shape[0], generator=g)
+    for into in (None, "scores"):
+        want, bound = reference(s, t, None, True, 1.0, gr)
+        for a, w, e, name in zip(run(s, t, None, True, 1.0, gr, into=into), want, bound, ("loss", "ds")):
+            check(a, w, e, F32, name)
