@@ -366,6 +366,9 @@ _TYPES = {torch.bfloat16: BF16, torch.float32: FP32}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_I32_MAX = 2 ** 31 - 1
+
+
 def _rows(t, name, index, n=None, d=None, dtype=None):
     """Row stride of a 2-D matrix that the library can read in place: adjacent values along a row, on the
     CUDA device `index`."""
@@ -373,6 +376,8 @@ def _rows(t, name, index, n=None, d=None, dtype=None):
     if len(shape) != 2 or (n is not None and (shape[0] != n or shape[1] != d)):
         raise ValueError(f"{name}: expected a 2-D tensor{'' if n is None else f' of shape {(n, d)}'}, "
                          f"got {tuple(shape)}")
+    if shape[1] > _I32_MAX:   # (the library counts them in 32 bits, and ctypes would cut the number)
+        raise ValueError(f"{name}: rows of {shape[1]} values are too long")
     if t.dtype not in _TYPES if dtype is None else t.dtype != dtype:
         raise ValueError(f"{name}: {t.dtype} is not supported here")
     if t.get_device() != index:
@@ -481,6 +486,8 @@ def distill_topk(scores, teacher, lists=None, kind: int = TEACHER_LOGITS, temper
     dev = _device(scores)
     ld_s = _rows(scores, "scores", dev, dtype=torch.float32)
     n, k = scores.shape
+    if n > _I32_MAX:
+        raise ValueError(f"scores: {n} rows are too many")
     ld_t = _rows(teacher, "teacher", dev, n, k)
     lp, ld_l = (None, 0) if lists is None else (lists.data_ptr(), _rows(lists, "lists", dev, n, k, torch.int32))
     g = _dense(grad_loss, "grad_loss", dev, (n,), torch.float32)

@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(NT) distill_kernel(const __grid_constant__ Dis
     const int32_t* lp = a.list ? a.list + (int64_t)row * a.ld_list : nullptr;
     // columns are taken from the 4-place boundary at or before the row's start, so that rows of an odd
     // stride still move 16 bytes at a time (single places cost twice the time)
-    const int c0 = EDGE ? -((a.off0 + row * a.off_step) & 3) : 0;
+    const int c0 = EDGE ? -int((a.off0 + (int64_t)row * a.off_step) & 3) : 0;
     float s[NV][VEC], f[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {

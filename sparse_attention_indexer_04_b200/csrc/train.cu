@@ -131,7 +131,8 @@ template <typename TT, bool WEIGHTS, int VEC, bool EDGE, int T, int NV, int NT>
 dsa_status distill_launch(const DistillArgs& a, cudaStream_t st)
 {
     constexpr int R = NT / T;
-    DSA_LAUNCH(kProfDistill, st, distill_kernel<TT, WEIGHTS, VEC, EDGE, T, NV, NT><<<(a.n + R - 1) / R, NT, 0, st>>>(a));
+    DSA_LAUNCH(kProfDistill, st, distill_kernel<TT, WEIGHTS, VEC, EDGE, T, NV, NT>
+               <<<(unsigned)((int64_t(a.n) + R - 1) / R), NT, 0, st>>>(a));
     return launched();
 }
 
@@ -160,7 +161,7 @@ dsa_status distill_pick(const DistillArgs& a, cudaStream_t st)
 {
     // 16 places a thread or so: with 8 the two joint reductions were a third of the instructions
     constexpr int U = 4 / VEC;   // registers' worth of a 4-wide load
-    const int32_t k = EDGE ? a.k + 3 : a.k;   // columns from the boundary before the row
+    const int64_t k = int64_t(a.k) + (EDGE ? 3 : 0);   // columns from the boundary before the row
     if (k <= 128) return distill_launch<TT, WEIGHTS, VEC, EDGE, 32, 1 * U, 256>(a, st);
     if (k <= 512) return distill_launch<TT, WEIGHTS, VEC, EDGE, 32, 4 * U, 256>(a, st);
     // many rows: the next one read ahead, with as many CTAs an SM as hold rows of 64 KB together

@@ -212,3 +212,26 @@ def test_weights_of_any_scale(k, tt):
         want, bound = reference(s, t, None, True, 1.0, gr)
         for a, w, e, name in zip(run(s, t, None, True, 1.0, gr, into=into), want, bound, ("loss", "ds")):
             check(a, w, e, F32, name)
+
+
+def test_a_row_as_long_as_lengths_go():
+    """k = 2^31 - 3, off the 4-place boundaries: one score row of 8.6 GB, the gradient over it.  Scores are equal and
+    the teacher's weight lies on the last place: q = 1/k, loss = log k.  A thread's sum counts to 2^22 in ones
+    (exact); the joining, the logarithms and the quotient round 20 times at most."""
+    k = 2 ** 31 - 3
+    s = torch.zeros(1, k, device=DEV)
+    t = torch.zeros(1, k, dtype=BF, device=DEV)
+    t[0, -1] = 3.0
+    loss, ds = dsa.distill_topk(s, t, kind=dsa.TEACHER_WEIGHTS, dscores=s)
+    assert abs(float(loss) - math.log(k)) <= 20 * U * math.log(k)
+    assert bool((ds[0, :-1] - 1.0 / k).abs().amax() <= 20 * U / k)
+    assert abs(float(ds[0, -1]) - (1.0 / k - 1.0)) <= 4 * U
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """The library counts a row's places in 32 bits: longer ones are refused, not cut."""
+    x = torch.empty(1, 2 ** 31, device=DEV)
+    y = x.view(BF)[:, :2 ** 31]
+    for bad in (lambda: dsa.distill_topk(x, y), lambda: dsa.distill_topk(x.t(), y.t()), lambda: dsa.layer_norm(y)):
+        with pytest.raises(ValueError):
+            bad()
