@@ -188,6 +188,32 @@ def _bytes(ws):
     return ctypes.c_size_t(ws.numel() * ws.element_size())
 
 
+def _tensors(x):
+    """The CUDA tensors of an argument or a result."""
+    if isinstance(x, torch.Tensor):
+        return [x] if x.is_cuda else []
+    if isinstance(x, Layout):
+        return _tensors([x.q_off, x.k_off, x.q_pos])
+    return [t for y in x for t in _tensors(y)] if isinstance(x, (list, tuple)) else []
+
+
+def _on_stream(stream, index, call, *args):
+    """call(*args) with `stream`, of the CUDA device `index`, as the current one.  Outputs and workspaces are then
+    made from that stream's memory: from the caller's stream's, they could be blocks that work pending there still
+    uses.  The allocator learns that the arguments are in use on `stream` and the results on the caller's."""
+    if stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+    caller = torch.cuda.current_stream(index)
+    with torch.cuda.stream(stream):
+        out = call(*args)
+    for t in _tensors(args):
+        t.record_stream(stream)
+    for t in _tensors(out):
+        t.record_stream(stream)
+        t.record_stream(caller)
+    return out
+
+
 # ------------------------------------------------------------------- dense
 
 def index_scores_workspace(layout: Layout) -> int:
@@ -196,12 +222,14 @@ def index_scores_workspace(layout: Layout) -> int:
 
 def index_scores(layout: Layout, Q, K, W, S=None, ws=None, stream=None):
     """Dense indexer scores: S [n_q, ld] fp32, -inf where the key is not eligible."""
+    if stream is not None:
+        return _on_stream(stream, layout.q_off.get_device(), index_scores, layout, Q, K, W, S, ws)
     if S is None:
         S = torch.empty(layout.num_queries, max(layout.max_keys, 1), dtype=torch.float32, device=layout.device)
     ws = _workspace(index_scores_workspace(layout), layout.device, ws)
     _check(_lib.dsa_index_scores(layout.ref(), _ptr(Q), _ptr(K), _ptr(W), _ptr(S), S.stride(0), _ptr(ws),
-                                 _bytes(ws), _stream(stream)), "dsa_index_scores")
-    _after(ws, "dsa_index_scores", stream)
+                                 _bytes(ws), _stream()), "dsa_index_scores")
+    _after(ws, "dsa_index_scores")
     return S
 
 
@@ -211,14 +239,17 @@ def index_topk_workspace(layout: Layout, k: int) -> int:
 
 def index_topk(layout: Layout, Q, K, W, k: int, idx=None, scores=None, want_scores=False, ws=None, stream=None):
     """Dense indexer top-k: idx [n_q, k] int32 (ascending, -1 padded), optional scores [n_q, k]."""
+    if stream is not None:
+        return _on_stream(stream, layout.q_off.get_device(), index_topk, layout, Q, K, W, k, idx, scores,
+                          want_scores, ws)
     if idx is None:
         idx = torch.empty(layout.num_queries, k, dtype=torch.int32, device=layout.device)
     if want_scores and scores is None:
         scores = torch.empty(layout.num_queries, k, dtype=torch.float32, device=layout.device)
     ws = _workspace(index_topk_workspace(layout, k), layout.device, ws)
     _check(_lib.dsa_index_topk(layout.ref(), _ptr(Q), _ptr(K), _ptr(W), k, _ptr(idx), _ptr(scores), _ptr(ws),
-                               _bytes(ws), _stream(stream)), "dsa_index_topk")
-    _after(ws, "dsa_index_topk", stream)
+                               _bytes(ws), _stream()), "dsa_index_topk")
+    _after(ws, "dsa_index_topk")
     return (idx, scores) if want_scores else idx
 
 
@@ -231,6 +262,9 @@ def index_layers(layout: Layout, Qs, Ks, Ws, k: int, retain_every: int = 1, lag:
                  ws=None, stream=None, side_stream=None):
     """Selections of len(Qs) layers (dsa_index_layers): idx[l] [n_q, k] int32 for layer l.  `events`: optional
     torch.cuda.Event per layer, recorded once idx[l] is complete (then `stream` is not made to wait)."""
+    if stream is not None:
+        return _on_stream(stream, layout.q_off.get_device(), index_layers, layout, Qs, Ks, Ws, k, retain_every, lag,
+                          idx, events, ws, None, side_stream)
     n = len(Qs)
     if not (len(Ks) == len(Ws) == n):
         raise ValueError("one Q, K and W per layer")
@@ -242,12 +276,12 @@ def index_layers(layout: Layout, Qs, Ks, Ws, k: int, retain_every: int = 1, lag:
     ev = None
     if events is not None:
         for e in events:
-            e.record(stream if stream is not None else torch.cuda.current_stream())   # creates the event
+            e.record()   # creates the event
         ev = (_P * n)(*[e.cuda_event for e in events])
     ws = _workspace(int(_lib.dsa_index_layers_workspace(layout.ref(), k)), layout.device, ws)
     _check(_lib.dsa_index_layers(layout.ref(), n, arr(Qs), arr(Ks), arr(Ws), k, retain_every, lag, arr(idx), ev,
-                                 _ptr(ws), _bytes(ws), _stream(stream), _stream(side_stream)), "dsa_index_layers")
-    _after(ws, "dsa_index_layers", stream)
+                                 _ptr(ws), _bytes(ws), _stream(), _stream(side_stream)), "dsa_index_layers")
+    _after(ws, "dsa_index_layers")
     return idx
 
 
@@ -274,12 +308,15 @@ def index_topk_host(layout: Layout, q_pos, Q, K, W, k: int, idx, ws, stream=None
 def index_topk_static(layout: Layout, Q, K, W, k: int, idx=None, scores=None, want_scores=False, stream=None):
     """dsa_index_topk with the library's built-in device scratch instead of a workspace (allocates nothing
     in the library; for callers that cannot allocate).  Calls on one device must not overlap on the GPU."""
+    if stream is not None:
+        return _on_stream(stream, layout.q_off.get_device(), index_topk_static, layout, Q, K, W, k, idx, scores,
+                          want_scores)
     if idx is None:
         idx = torch.empty(layout.num_queries, k, dtype=torch.int32, device=layout.device)
     if want_scores and scores is None:
         scores = torch.empty(layout.num_queries, k, dtype=torch.float32, device=layout.device)
     _check(_lib.dsa_index_topk_static(layout.ref(), _ptr(Q), _ptr(K), _ptr(W), k, _ptr(idx), _ptr(scores),
-                                      _stream(stream)), "dsa_index_topk_static")
+                                      _stream()), "dsa_index_topk_static")
     return (idx, scores) if want_scores else idx
 
 
@@ -300,14 +337,17 @@ def pivot_group_index_workspace(layout: Layout, k: int, group: int, n_cand: int,
 def pivot_group_index(layout: Layout, Q, K, W, k: int, group: int, n_cand: int, mode: int, idx=None, cand=None,
                       want_cand=False, ws=None, stream=None):
     """PIVOT Reuse (mode 0) / Refine (mode 1): idx [n_q, k]; optional cand [n_groups, n_cand]."""
+    if stream is not None:
+        return _on_stream(stream, layout.q_off.get_device(), pivot_group_index, layout, Q, K, W, k, group, n_cand,
+                          mode, idx, cand, want_cand, ws)
     if idx is None:
         idx = torch.empty(layout.num_queries, k, dtype=torch.int32, device=layout.device)
     if want_cand and cand is None:
         cand = torch.empty(max(pivot_num_groups(layout, group), 0), n_cand, dtype=torch.int32, device=layout.device)
     ws = _workspace(pivot_group_index_workspace(layout, k, group, n_cand, mode), layout.device, ws)
     _check(_lib.pivot_group_index(layout.ref(), _ptr(Q), _ptr(K), _ptr(W), k, group, n_cand, mode, _ptr(idx),
-                                  _ptr(cand), _ptr(ws), _bytes(ws), _stream(stream)), "pivot_group_index")
-    _after(ws, "pivot_group_index", stream)
+                                  _ptr(cand), _ptr(ws), _bytes(ws), _stream()), "pivot_group_index")
+    _after(ws, "pivot_group_index")
     return (idx, cand) if want_cand else idx
 
 
@@ -317,13 +357,16 @@ def pivot_refine_candidates_workspace(layout: Layout, k: int, group: int, n_cand
 
 def pivot_refine_candidates(layout: Layout, Q, K, W, k: int, group: int, cand, idx=None, ws=None, stream=None):
     """Refine on supplied candidates: cand [n_groups, n_cand] int32 (ascending, -1 padded) -> idx [n_q, k]."""
+    if stream is not None:
+        return _on_stream(stream, layout.q_off.get_device(), pivot_refine_candidates, layout, Q, K, W, k, group,
+                          cand, idx, ws)
     n_cand = int(cand.shape[1])
     if idx is None:
         idx = torch.empty(layout.num_queries, k, dtype=torch.int32, device=layout.device)
     ws = _workspace(pivot_refine_candidates_workspace(layout, k, group, n_cand), layout.device, ws)
     _check(_lib.pivot_refine_candidates(layout.ref(), _ptr(Q), _ptr(K), _ptr(W), k, group, n_cand, _ptr(cand),
-                                        _ptr(idx), _ptr(ws), _bytes(ws), _stream(stream)), "pivot_refine_candidates")
-    _after(ws, "pivot_refine_candidates", stream)
+                                        _ptr(idx), _ptr(ws), _bytes(ws), _stream()), "pivot_refine_candidates")
+    _after(ws, "pivot_refine_candidates")
     return idx
 
 
@@ -335,10 +378,12 @@ def hisa_num_blocks(layout: Layout, block: int) -> int:
 
 def hisa_pool_keys(layout: Layout, K, block: int, pooled=None, stream=None):
     """Mean-pooled block keys [n_blocks, d] fp32."""
+    if stream is not None:
+        return _on_stream(stream, layout.q_off.get_device(), hisa_pool_keys, layout, K, block, pooled)
     if pooled is None:
         pooled = torch.empty(max(hisa_num_blocks(layout, block), 0), layout.head_dim, dtype=torch.float32,
                              device=layout.device)
-    _check(_lib.hisa_pool_keys(layout.ref(), _ptr(K), block, _ptr(pooled), _stream(stream)), "hisa_pool_keys")
+    _check(_lib.hisa_pool_keys(layout.ref(), _ptr(K), block, _ptr(pooled), _stream()), "hisa_pool_keys")
     return pooled
 
 
@@ -349,14 +394,17 @@ def hisa_index_workspace(layout: Layout, k: int, block: int, keep: int) -> int:
 def hisa_index(layout: Layout, Q, K, W, pooled, k: int, block: int, keep: int, idx=None, kept=None,
                want_kept=False, ws=None, stream=None):
     """HISA top-k: idx [n_q, k]; optional kept [n_q, keep+2] block lists."""
+    if stream is not None:
+        return _on_stream(stream, layout.q_off.get_device(), hisa_index, layout, Q, K, W, pooled, k, block, keep,
+                          idx, kept, want_kept, ws)
     if idx is None:
         idx = torch.empty(layout.num_queries, k, dtype=torch.int32, device=layout.device)
     if want_kept and kept is None:
         kept = torch.empty(layout.num_queries, keep + 2, dtype=torch.int32, device=layout.device)
     ws = _workspace(hisa_index_workspace(layout, k, block, keep), layout.device, ws)
     _check(_lib.hisa_index(layout.ref(), _ptr(Q), _ptr(K), _ptr(W), _ptr(pooled), k, block, keep, _ptr(idx),
-                           _ptr(kept), _ptr(ws), _bytes(ws), _stream(stream)), "hisa_index")
-    _after(ws, "hisa_index", stream)
+                           _ptr(kept), _ptr(ws), _bytes(ws), _stream()), "hisa_index")
+    _after(ws, "hisa_index")
     return (idx, kept) if want_kept else idx
 
 
@@ -409,32 +457,23 @@ def _device(t):
     return t.get_device()
 
 
-def _on(index, call, *args, stream=None):
-    """call(*args, stream) with the CUDA device `index` current; stream: that device's current one by default."""
+def _on(index, call, *args):
+    """call(*args, stream) with the CUDA device `index` current and that device's current stream."""
     if index != torch.cuda.current_device():
         with torch.cuda.device(index):
-            return _on(index, call, *args, stream=stream)
-    if stream is not None:
-        raw = stream.cuda_stream
-    elif _raw_stream is not None:
+            return _on(index, call, *args)
+    if _raw_stream is not None:
         raw = _raw_stream(index)
     else:
         raw = torch.cuda.current_stream(index).cuda_stream
     return call(*args, raw)
 
 
-def _used_on(stream, *made):
-    """Tells the allocator that tensors made here on the current stream are in use on `stream`: their memory is
-    not handed out again before that stream's work so far is done."""
-    if stream is not None:
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
-
-
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, out_dtype=None, want_stats=False, stream=None):
     """Layer norm of the rows of x [n, d] (bf16 or fp32; rows may be a slice of a wider matrix): y [n, d] of
     out_dtype (x's by default); with want_stats also mean and rstd [n] fp32, which the backward pass takes."""
+    if stream is not None:
+        return _on_stream(stream, _device(x), layer_norm, x, weight, bias, eps, out, out_dtype, want_stats)
     dev = _device(x)
     ld_x = _rows(x, "x", dev)
     n, d = x.shape
@@ -447,8 +486,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-6, out=None, out_dtype
         mean, rstd = x.new_empty(n, dtype=torch.float32), x.new_empty(n, dtype=torch.float32)
         mp, rp = mean.data_ptr(), rstd.data_ptr()
     _check(_on(dev, _lib.dsa_layer_norm, n, d, x.data_ptr(), _TYPES[x.dtype], ld_x, w, b, eps, out.data_ptr(),
-               _TYPES[out.dtype], ld_y, mp, rp, stream=stream), "dsa_layer_norm")
-    _used_on(stream, out, mean, rstd)
+               _TYPES[out.dtype], ld_y, mp, rp), "dsa_layer_norm")
     return (out, mean, rstd) if want_stats else out
 
 
@@ -459,6 +497,8 @@ def layer_norm_backward_workspace(n: int, d: int) -> int:
 
 def layer_norm_backward(dy, x, weight, mean, rstd, dx=None, ws=None, stream=None):
     """Backward pass of layer_norm: (dx [n, d] of x's type, dweight [d], dbias [d] fp32)."""
+    if stream is not None:
+        return _on_stream(stream, _device(x), layer_norm_backward, dy, x, weight, mean, rstd, dx, ws)
     dev = _device(x)
     ld_x = _rows(x, "x", dev)
     n, d = x.shape
@@ -473,8 +513,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, dx=None, ws=None, stream=None
         ws = _workspace(layer_norm_backward_workspace(n, d), x.device)
     _check(_on(dev, _lib.dsa_layer_norm_backward, n, d, dy.data_ptr(), _TYPES[dy.dtype], ld_dy, x.data_ptr(),
                _TYPES[x.dtype], ld_x, w, mp, rp, dx.data_ptr(), ld_dx, dw.data_ptr(), db.data_ptr(), ws.data_ptr(),
-               ws.numel() * ws.element_size(), stream=stream), "dsa_layer_norm_backward")
-    _used_on(stream, dx, dw, db, ws)
+               ws.numel() * ws.element_size()), "dsa_layer_norm_backward")
     return dx, dw, db
 
 
@@ -483,6 +522,9 @@ def distill_topk(scores, teacher, lists=None, kind: int = TEACHER_LOGITS, temper
     """Distillation loss of each row's scores [n, k] from a teacher's logits or weights on the same places, and
     its gradient: (loss [n], dscores [n, k]).  Places with a negative entry in `lists` or a score of -inf do not
     count.  grad_loss [n]: the gradient of each row's loss (ones by default)."""
+    if stream is not None:
+        return _on_stream(stream, _device(scores), distill_topk, scores, teacher, lists, kind, temperature,
+                          grad_loss, loss, dscores)
     dev = _device(scores)
     ld_s = _rows(scores, "scores", dev, dtype=torch.float32)
     n, k = scores.shape
@@ -498,8 +540,7 @@ def distill_topk(scores, teacher, lists=None, kind: int = TEACHER_LOGITS, temper
     ld_d = _rows(dscores, "dscores", dev, n, k, torch.float32)
     _check(_on(dev, _lib.dsa_distill_topk, n, k, scores.data_ptr(), ld_s, lp, ld_l, teacher.data_ptr(),
                _TYPES[teacher.dtype], ld_t, kind, temperature, g, _dense(loss, "loss", dev, (n,), torch.float32),
-               dscores.data_ptr(), ld_d, stream=stream), "dsa_distill_topk")
-    _used_on(stream, loss, dscores)
+               dscores.data_ptr(), ld_d), "dsa_distill_topk")
     return loss, dscores
 
 
@@ -525,16 +566,17 @@ def list_scores_workspace(layout: Layout, k: int) -> int:
 def list_scores(layout: Layout, Q, K, W, lists, scores=None, ws=None, stream=None):
     """Indexer scores at listed keys: lists [n_q, k] int32 (ascending, -1 padded) -> scores [n_q, k] fp32, -inf
     where a place is empty or its key is not in the query's prefix."""
+    if stream is not None:
+        return _on_stream(stream, _device(Q), list_scores, layout, Q, K, W, lists, scores, ws)
     dev, k, q, kk, w, l = _list_inputs(layout, Q, K, W, lists)
     if scores is None:
         scores = W.new_empty(lists.shape)
     if ws is None:
         ws = _workspace(list_scores_workspace(layout, k), Q.device)
     _check(_on(dev, _lib.dsa_list_scores, layout.ref(), q, kk, w, k, l,
-               _dense(scores, "scores", dev, lists.shape, torch.float32), ws.data_ptr(), ws.numel() * ws.element_size(),
-               stream=stream), "dsa_list_scores")
-    _used_on(stream, scores, ws)
-    _after(ws, "dsa_list_scores", stream)
+               _dense(scores, "scores", dev, lists.shape, torch.float32), ws.data_ptr(), ws.numel() * ws.element_size()),
+           "dsa_list_scores")
+    _after(ws, "dsa_list_scores")
     return scores
 
 
@@ -544,6 +586,8 @@ def list_scores_backward_workspace(layout: Layout, k: int) -> int:
 
 def list_scores_backward(layout: Layout, Q, K, W, lists, dscores, dQ=None, dK=None, dW=None, ws=None, stream=None):
     """Backward pass of list_scores: (dQ [n_q, H, d] bf16, dK [n_k, d] bf16, dW [n_q, H] fp32)."""
+    if stream is not None:
+        return _on_stream(stream, _device(Q), list_scores_backward, layout, Q, K, W, lists, dscores, dQ, dK, dW, ws)
     dev, k, q, kk, w, l = _list_inputs(layout, Q, K, W, lists)
     ds = _dense(dscores, "dscores", dev, lists.shape, torch.float32)
     dQ = torch.empty_like(Q) if dQ is None else dQ
@@ -553,10 +597,9 @@ def list_scores_backward(layout: Layout, Q, K, W, lists, dscores, dQ=None, dK=No
         ws = _workspace(list_scores_backward_workspace(layout, k), Q.device)
     _check(_on(dev, _lib.dsa_list_scores_backward, layout.ref(), q, kk, w, k, l, ds,
                _dense(dQ, "dQ", dev, Q.shape, torch.bfloat16), _dense(dK, "dK", dev, K.shape, torch.bfloat16),
-               _dense(dW, "dW", dev, W.shape, torch.float32), ws.data_ptr(), ws.numel() * ws.element_size(),
-               stream=stream), "dsa_list_scores_backward")
-    _used_on(stream, dQ, dK, dW, ws)
-    _after(ws, "dsa_list_scores_backward", stream)
+               _dense(dW, "dW", dev, W.shape, torch.float32), ws.data_ptr(), ws.numel() * ws.element_size()),
+           "dsa_list_scores_backward")
+    _after(ws, "dsa_list_scores_backward")
     return dQ, dK, dW
 
 
