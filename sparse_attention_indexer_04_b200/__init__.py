@@ -282,6 +282,9 @@ def index_layers(layout: Layout, Qs, Ks, Ws, k: int, retain_every: int = 1, lag:
     _check(_lib.dsa_index_layers(layout.ref(), n, arr(Qs), arr(Ks), arr(Ws), k, retain_every, lag, arr(idx), ev,
                                  _ptr(ws), _bytes(ws), _stream(), _stream(side_stream)), "dsa_index_layers")
     _after(ws, "dsa_index_layers")
+    if events is not None:   # (else this stream waits for the side stream, and later work here comes after it)
+        for t in _tensors([layout, Qs, Ks, Ws, ws, idx]):
+            t.record_stream(side_stream)
     return idx
 
 

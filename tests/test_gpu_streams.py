@@ -132,3 +132,27 @@ def test_a_stream_of_another_device_is_refused():
     for name, call in calls().items():
         with pytest.raises(ValueError):
             call(stream=elsewhere)
+
+
+def test_the_side_stream_of_several_layers_keeps_its_memory():
+    """With an event per layer the caller's stream does not wait for the side stream, which still works on the
+    inputs, the workspace and the rows when the call has returned."""
+    b = workloads.ragged(9, [300, 200], [300, 900], H=64, d=128, k=64, integer=False)
+    lay = dsa.Layout.from_batch(b, DEV)
+    Q, K, W = b.Q.to(DEV), b.K.to(DEV), b.W.to(DEV)
+    want = dsa.index_topk(lay, Q, K, W, 64)
+    side, slow = torch.cuda.Stream(DEV), Slow()
+    torch.cuda.synchronize()
+    for _ in range(2):
+        events = [torch.cuda.Event() for _ in range(4)]
+        held = [[t.clone() for _ in range(4)] for t in (Q, K, W)]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            slow()
+        got = dsa.index_layers(lay, *held, 64, retain_every=2, events=events, side_stream=side)
+        del held
+        junk = [torch.full((2 ** e,), 255, dtype=torch.uint8, device=DEV) for e in range(9, 26) for _ in range(4)]
+        torch.cuda.synchronize()
+        for t in got:
+            assert torch.equal(t, want)
+        del junk
