@@ -225,9 +225,11 @@ constexpr int32_t kRowsMaxQueries = 32768;   // (counts of 16 bits)
 constexpr size_t kPartsBudget = size_t(4096) << 20;
 
 // What a batch's lists hold, as far as the host knows: the queries of a sequence taken as its last ones
-// (a training batch: all of them; a chunk at the end of a context).
+// (a training batch: all of them; a chunk at the end of a context), those above its keys' number with the
+// whole of it.
 struct ListWork {
     double listed = 0;   // listed (query, key) pairs
+    double empty = 0;    // places of the tiles of 128 that lists end in, behind their ends
     double dense = 0;    // eligible pairs
     double blocks = 0;   // (query, key block) pairs with a listed key
 };
@@ -237,27 +239,35 @@ ListWork list_work(const dsa_batch* b, int32_t k)
     ListWork w;
     for (int i = 0; i < b->num_seqs; ++i) {
         const double L = b->k_offsets_host[i + 1] - b->k_offsets_host[i];
-        const double nq = std::min<double>(b->q_offsets_host[i + 1] - b->q_offsets_host[i], L);
+        const double all = b->q_offsets_host[i + 1] - b->q_offsets_host[i], nq = std::min(all, L);
         const double p0 = L - nq + 1, p1 = L;   // prefix lengths from p0 to p1
         // sums over p0 .. p1 of p, of min(k, p) and of the blocks they touch
         const auto sum = [](double lo, double hi) { return hi < lo ? 0. : (lo + hi) * (hi - lo + 1) / 2; };
         const double m = std::min<double>(k, p1), dense = sum(p0, p1);
-        const double listed = sum(p0, std::min(m, p1)) + std::max(0., p1 - std::max(p0 - 1, m)) * k;
-        w.dense += dense;
-        w.listed += listed;
-        w.blocks += std::min(listed, dense / kDkKeys + nq / 2);
+        const double whole = std::max(0., p1 - std::max(p0 - 1, m));   // queries of k places
+        const double listed = sum(p0, std::min(m, p1)) + whole * k;
+        const double full = std::min<double>(k, L);   // places of a query with the whole prefix
+        const auto rest = [](double places) { return std::ceil(places / 128) * 128 - places; };
+        w.dense += dense + (all - nq) * L;
+        w.listed += listed + (all - nq) * full;
+        w.empty += whole * rest(k) + (nq - whole) * 64 + (all - nq) * rest(full);
+        w.blocks += std::min(listed, dense / kDkKeys + nq / 2) + (all - nq) * std::min(full, std::ceil(L / kDkKeys));
     }
     return w;
 }
 
 // Whether dK is summed from one row per listed pair or from dense products over whole key blocks.
-// Measured at d = 128, in ns: a row 0.22 (written by the dQ pass, read once), a key 0.16 and four more
-// launches 15,000; a (query, block) product 6.8 with 64 heads, 2.5 with 8, 1.2 with 4, a block's CTA 70.
+// Measured both ways over 35 sizes (512 to 33,000 queries, 600 to 32K keys, 1 to 512 places) with H, d of
+// 4, 32; 4, 128; 16, 64 and 64, 128, in ns: a row 0.2 at d = 128 (written by the dQ pass, read once), an empty
+// place of a tile 0.02 and as much again at d = 128; a (query, block) product 0.3 and 4.3 with 64 heads, a
+// block's CTA 150 and 350 at d = 128.  The form taken so is 0.5 % slower than the better one on average, 21 %
+// at most.
 bool dk_by_rows(const dsa_batch* b, int32_t k)
 {
     const ListWork w = list_work(b, k);
-    const double units = b->num_keys / kDkKeys + b->num_seqs;
-    return w.listed * 0.22 + b->num_keys * 0.16 + 15000 < w.blocks * (1.2 + 5.6 * b->num_heads / 64.) + units * 70;
+    const double units = b->num_keys / kDkKeys + b->num_seqs, d = b->head_dim / 128.;
+    return w.listed * 0.2 * d + w.empty * (0.02 + 0.02 * d) <
+           w.blocks * (0.3 + 4.3 * b->num_heads / 64.) + units * (150 + 350 * d);
 }
 
 // Whether the listed scores are picked from all scores of the prefix or computed from gathered keys.
