@@ -338,6 +338,11 @@ dsa_status dsa_distill_topk(int32_t n, int32_t k, const float* scores, int64_t l
  * Requires 1 <= k <= 16384.  The listed keys are gathered, or, where lists
  * cover much of their prefixes, picked from all its scores (at most 4 GiB of
  * the workspace); the choice depends on the sizes alone.
+ * Values that are not finite in a listed key, or in Q or W of a query with a
+ * list, give the scores and gradients that the formulas carry them to, with
+ * max(0, NaN) = NaN; where dK is taken from products over whole blocks of 256
+ * keys, a query whose Q or W is not finite may make NaN of dK of any key in a
+ * block that it lists.  Those of keys that no query lists have no effect.
  */
 size_t dsa_list_scores_workspace(const dsa_batch* batch, int32_t k);
 dsa_status dsa_list_scores(const dsa_batch* batch, const void* Q, const void* K, const float* W, int32_t k,

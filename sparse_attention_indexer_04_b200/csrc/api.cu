@@ -308,7 +308,7 @@ int32_t tc_unit_capacity(const TcSource& src, int32_t n_rows, int32_t chunk, int
 
 template <int D, int H>
 dsa_status launch_tc_shape(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mkg, const TcArgs& a,
-                           const DenseSetupArgs& su, int32_t n_units, int n_acc, cudaStream_t st)
+                           const DenseSetupArgs& su, int32_t n_units, int n_acc, bool keep_nan, cudaStream_t st)
 {
     using SH = TcShape<D, H>;
     const int budget = 232448;
@@ -329,25 +329,26 @@ dsa_status launch_tc_shape(const CUtensorMap& mq, const CUtensorMap& mk, const C
         DSA_LAUNCH(kProfScoreTc, st, launch_pdl(latency_bound(n_units), score_tc_kernel<D, H, kTcBlocks>, n_units,
                                                 kTcThreadsTiles, smem, st, mq, mk, mkg, args, su));
     } else {
-        if ((s = set_smem(score_tc_kernel<D, H, kTcTiles>, smem)) != DSA_OK) return s;
-        DSA_LAUNCH(kProfScoreTc, st, launch_pdl(latency_bound(n_units), score_tc_kernel<D, H, kTcTiles>, n_units,
-                                                kTcThreadsTiles, smem, st, mq, mk, mkg, args, su));
+        const auto kern = keep_nan ? score_tc_kernel<D, H, kTcTilesNan> : score_tc_kernel<D, H, kTcTiles>;
+        if ((s = set_smem(kern, smem)) != DSA_OK) return s;
+        DSA_LAUNCH(kProfScoreTc, st, launch_pdl(latency_bound(n_units), kern, n_units, kTcThreadsTiles, smem, st, mq,
+                                                mk, mkg, args, su));
     }
     return launched();
 }
 
 template <int D>
 dsa_status launch_tc_d(int H, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mkg, const TcArgs& a,
-                       const DenseSetupArgs& su, int32_t n_units, int n_acc, cudaStream_t st)
+                       const DenseSetupArgs& su, int32_t n_units, int n_acc, bool keep_nan, cudaStream_t st)
 {
     switch (H) {
-    case 1: return launch_tc_shape<D, 1>(mq, mk, mkg, a, su, n_units, n_acc, st);
-    case 2: return launch_tc_shape<D, 2>(mq, mk, mkg, a, su, n_units, n_acc, st);
-    case 4: return launch_tc_shape<D, 4>(mq, mk, mkg, a, su, n_units, n_acc, st);
-    case 8: return launch_tc_shape<D, 8>(mq, mk, mkg, a, su, n_units, n_acc, st);
-    case 16: return launch_tc_shape<D, 16>(mq, mk, mkg, a, su, n_units, n_acc, st);
-    case 32: return launch_tc_shape<D, 32>(mq, mk, mkg, a, su, n_units, n_acc, st);
-    default: return launch_tc_shape<D, 64>(mq, mk, mkg, a, su, n_units, n_acc, st);
+    case 1: return launch_tc_shape<D, 1>(mq, mk, mkg, a, su, n_units, n_acc, keep_nan, st);
+    case 2: return launch_tc_shape<D, 2>(mq, mk, mkg, a, su, n_units, n_acc, keep_nan, st);
+    case 4: return launch_tc_shape<D, 4>(mq, mk, mkg, a, su, n_units, n_acc, keep_nan, st);
+    case 8: return launch_tc_shape<D, 8>(mq, mk, mkg, a, su, n_units, n_acc, keep_nan, st);
+    case 16: return launch_tc_shape<D, 16>(mq, mk, mkg, a, su, n_units, n_acc, keep_nan, st);
+    case 32: return launch_tc_shape<D, 32>(mq, mk, mkg, a, su, n_units, n_acc, keep_nan, st);
+    default: return launch_tc_shape<D, 64>(mq, mk, mkg, a, su, n_units, n_acc, keep_nan, st);
     }
 }
 
@@ -358,6 +359,7 @@ struct TcOpts {
     int64_t plane_rows = 0;
     int32_t min_tiles = 8;      // key tiles per unit at least (tc_splits)
     const DenseSetupArgs* own_setup = nullptr;   // dense launches of one wave: the kernel's own set-up
+    bool keep_nan = false;      // contiguous key tiles: a NaN product gives a NaN score
 };
 
 // Key tiles of a block map with whole 128-key tiles per block are contiguous: one tile load each.
@@ -412,9 +414,9 @@ dsa_status tc_score(const RowDesc* rows, int32_t n_rows, int32_t row_base, const
     static const DenseSetupArgs kNoSetup{};
     const DenseSetupArgs& su = o.own_setup ? *o.own_setup : kNoSetup;
     switch (D) {
-    case 32: return launch_tc_d<32>(H, mq, mk, mkg, a, su, tiles * splits, n_acc, st);
-    case 64: return launch_tc_d<64>(H, mq, mk, mkg, a, su, tiles * splits, n_acc, st);
-    default: return launch_tc_d<128>(H, mq, mk, mkg, a, su, tiles * splits, n_acc, st);
+    case 32: return launch_tc_d<32>(H, mq, mk, mkg, a, su, tiles * splits, n_acc, o.keep_nan, st);
+    case 64: return launch_tc_d<64>(H, mq, mk, mkg, a, su, tiles * splits, n_acc, o.keep_nan, st);
+    default: return launch_tc_d<128>(H, mq, mk, mkg, a, su, tiles * splits, n_acc, o.keep_nan, st);
     }
 }
 
@@ -968,9 +970,11 @@ dsa_status dense_scores(const dsa_batch* b, const HostInfo& hi, const void* Q, c
         b->q_offsets, b->k_offsets, b->q_pos, b->num_seqs, b->num_queries, p.rows));
     dsa_status s = launched();
     if (s != DSA_OK) return s;
+    TcOpts o;
+    o.keep_nan = true;
     const TcSource src{Q, b->num_queries, W, b->q_offsets, b->q_offsets_host, b->num_seqs};
     return tc_score(p.rows, b->num_queries, 0, src, b->num_heads, b->head_dim, K, b->num_keys, b->k_offsets, ColMap{},
-                    hi.max_k, S, score_ld(hi.max_k), p.units, p.tile_base, status, st);
+                    hi.max_k, S, score_ld(hi.max_k), p.units, p.tile_base, status, st, o);
 }
 
 }  // namespace dsa

@@ -599,6 +599,8 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
         const int lrow = quarter * 32 + lane;   // key of the tile
         const int st = threadIdx.x - 64 - set * 128;   // thread of the set
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        // head h's part of a score; the zero rows above H give NaN with an infinite key
+        [[maybe_unused]] auto relu = [&](int h, float x) { return relu_nan(HP > 16 || h < H ? x : 0.f); };
         int n = 0, it = 0, all = 0;
         bool alive = true;
         int nx = t0 < n_q ? a.l.rows[t0].ncols : 0, nx2 = t0 + step < n_q ? a.l.rows[t0 + step].ncols : 0;
@@ -657,8 +659,8 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
 #pragma unroll
                     for (int h = 0; h < HP; h += 4) {
                         const float4 w4 = *reinterpret_cast<const float4*>(w + h);
-                        acc = fma_f32x2(pack_f32x2(w4.x, w4.y), pack_f32x2(fmaxf(v[h], 0.f), fmaxf(v[h + 1], 0.f)), acc);
-                        acc = fma_f32x2(pack_f32x2(w4.z, w4.w), pack_f32x2(fmaxf(v[h + 2], 0.f), fmaxf(v[h + 3], 0.f)), acc);
+                        acc = fma_f32x2(pack_f32x2(w4.x, w4.y), pack_f32x2(relu(h, v[h]), relu(h + 1, v[h + 1])), acc);
+                        acc = fma_f32x2(pack_f32x2(w4.z, w4.w), pack_f32x2(relu(h + 2, v[h + 2]), relu(h + 3, v[h + 3])), acc);
                     }
                     float s0, s1;
                     unpack_f32x2(acc, s0, s1);
@@ -704,7 +706,7 @@ __global__ void __launch_bounds__(list_threads(MODE), 1)
                             for (int y = 0; y < 2; ++y) {
                                 const float s0 = v[h % CW + x + 2 * y], s1 = v[h % CW + x + 2 * y + 1];
                                 uint64_t& acc = dw[(h + x) / 2 + y];
-                                acc = fma_f32x2(ee, pack_f32x2(fmaxf(s0, 0.f), fmaxf(s1, 0.f)), acc);
+                                acc = fma_f32x2(ee, pack_f32x2(relu_nan(s0), relu_nan(s1)), acc);
                                 p[x / 2 + y] = relu_grad_pair(s0, s1, ee, y ? w2.y : w2.x);
                             }
                         }

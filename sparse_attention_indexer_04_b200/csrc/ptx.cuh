@@ -137,6 +137,14 @@ __device__ __forceinline__ void tma_gather4_2d(void* dst, const CUtensorMap* map
 // evicted after normal ones.
 // Two fp32 values as one 64-bit register pair, and back; d = a * b + c on both halves at once (each
 // half one IEEE fp32 fused multiply-add, rounded to nearest even).
+// max(0, x), with NaN for NaN (fmaxf gives 0).
+__device__ __forceinline__ float relu_nan(float x)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi)
 {
     uint64_t r;

@@ -103,9 +103,10 @@ __device__ __forceinline__ uint32_t dynamic_smem_size()
 
 // MODE kTcTiles: contiguous key tiles; kTcGather: the unit's key tiles are gathered through the
 // column map (a.gather == 1); kTcBlocks: contiguous tiles at computed rows, the three planes of
-// fp32 keys (a.planes) or whole 128-key tiles of a block map (a.block_tiles).  The cases are
-// compiled apart, so the dense scan keeps the leanest producer and MMA-issuer loops.
-enum : int { kTcTiles = 0, kTcGather = 1, kTcBlocks = 2 };
+// fp32 keys (a.planes) or whole 128-key tiles of a block map (a.block_tiles); kTcTilesNan: kTcTiles for
+// scores that are a result of their own, where a NaN product gives NaN and not, as in the rankings, 0.  The
+// cases are compiled apart, so the dense scan keeps the leanest producer and MMA-issuer loops.
+enum : int { kTcTiles = 0, kTcGather = 1, kTcBlocks = 2, kTcTilesNan = 3 };
 
 template <int D, int H, int MODE>
 __global__ void __launch_bounds__(MODE == kTcGather ? kTcThreads : kTcThreadsTiles, 1)
@@ -355,6 +356,7 @@ __global__ void __launch_bounds__(MODE == kTcGather ? kTcThreads : kTcThreadsTil
         __syncwarp();
     } else {   // warps 2..9
         // ---------------------------------------------------------- epilogue
+        const auto relu = [](float x) { return MODE == kTcTilesNan ? relu_nan(x) : fmaxf(x, 0.f); };
         // the tile's head weights and eligible counts, shared by the 8 epilogue warps
         for (int i = threadIdx.x - 64; i < 2 * NQA * H; i += 256) {
             const int j = i / H;
@@ -399,14 +401,14 @@ __global__ void __launch_bounds__(MODE == kTcGather ? kTcThreads : kTcThreadsTil
                         for (int h = 0; h < H; h += 4) {
                             const float4 w4 = *reinterpret_cast<const float4*>(w + h);
                             acc = fma_f32x2(pack_f32x2(w4.x, w4.y),
-                                            pack_f32x2(fmaxf(v[q * H + h], 0.f), fmaxf(v[q * H + h + 1], 0.f)), acc);
+                                            pack_f32x2(relu(v[q * H + h]), relu(v[q * H + h + 1])), acc);
                             acc = fma_f32x2(pack_f32x2(w4.z, w4.w),
-                                            pack_f32x2(fmaxf(v[q * H + h + 2], 0.f), fmaxf(v[q * H + h + 3], 0.f)), acc);
+                                            pack_f32x2(relu(v[q * H + h + 2]), relu(v[q * H + h + 3])), acc);
                         }
                         unpack_f32x2(acc, s0, s1);
                     } else {
 #pragma unroll
-                        for (int h = 0; h < H; ++h) s0 = fmaf(w[h], fmaxf(v[q * H + h], 0.f), s0);
+                        for (int h = 0; h < H; ++h) s0 = fmaf(w[h], relu(v[q * H + h]), s0);
                     }
                     if (j < u.nrows && key < sNc[j])   // streaming store: score rows are read once, later
                         __stcs(&a.S[(int64_t)(u.row0 + j) * a.ld_s + key], (s0 + s1) + 0.f);   // -0 -> +0

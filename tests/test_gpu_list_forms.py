@@ -1,5 +1,6 @@
 """Scores at listed keys in every form that the sizes choose between, each case asserting the form it took: scores
 gathered or picked from those of the whole prefix, dK from dense key blocks or from one row per listed pair."""
+import math
 import subprocess
 import sys
 
@@ -220,6 +221,91 @@ def test_both_forms_of_scores_agree():
     part = scores("gathered", few, Q[1480:1500].contiguous(), K[:1500], W[1480:1500].contiguous(),
                   lists[1480:1500].contiguous().to(DEV))
     assert torch.equal(whole[1480:1500], part)
+
+
+# -------------------------------------------------------------- no numbers
+
+NOT_FINITE = [("gathered", "dense", [300, 200], [400, 300], 4, 32, 200),
+              ("gathered", "dense", [300, 200], [300, 200], 64, 64, 150),
+              ("gathered", "rows", [60, 30], [200, 300], 4, 32, 40),
+              ("gathered", "rows", [60, 30], [9000, 6000], 64, 128, 40),
+              ("picked", "dense", [1500, 700], [1500, 700], 4, 128, 601)]
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("forward,form,q_lens,k_lens,H,d,k", NOT_FINITE)
+def test_a_key_that_is_not_finite(forward, form, q_lens, k_lens, H, d, k, value):
+    """It makes the scores that list it what the formula makes of them (NaN, or infinite), reaches dQ and dW of the
+    queries that list it, and nothing else; unlisted ones reach nothing."""
+    b = workloads.ragged(H + k, q_lens, k_lens, H=H, d=d, k=8, integer=False)
+    g = gen(k)
+    lists, ds = random_lists(g, b, k), randn(g, b.n_q, k)
+    lay, Q, K, W = on_gpu(b)
+    l, e = lists.to(DEV), ds.to(DEV)
+    want = dsa.list_scores(lay, Q, K, W, l)
+    bwd = dsa.list_scores_backward(lay, Q, K, W, l, e)
+    t = q_lens[0] - 2
+    bad = int(lists[t, lists[t] >= 0][3])            # a key of the first sequence
+    first = torch.zeros(b.n_q, dtype=torch.bool)
+    first[:q_lens[0]] = True
+    with_bad = ((lists == bad).any(1) & first).to(DEV)
+    at = (l == bad) & with_bad[:, None]
+    none = torch.ones(k_lens[0], dtype=torch.bool)
+    none[lists[:q_lens[0]][lists[:q_lens[0]] >= 0].long().unique()] = False
+    K2 = K.clone()
+    K2[bad, 1] = value
+    K2[:k_lens[0]][none.to(DEV)] = math.nan
+    s = scores(forward, lay, Q, K2, W, l)
+    assert torch.equal(s[~at], want[~at])
+    dot = torch.einsum("thd,d->th", Q.double(), K2[bad].double())
+    exact = torch.einsum("th,th->t", torch.relu(dot), W.double())[:, None].expand_as(s)[at]
+    assert torch.equal(torch.isnan(s[at]), torch.isnan(exact))
+    inf = torch.isinf(exact)
+    assert torch.equal(torch.isinf(s[at]), inf) and torch.equal(s[at][inf], exact.float()[inf])
+    got = backward(form, 1, lay, Q, K2, W, l, e)
+    assert torch.equal(got[0][~with_bad], bwd[0][~with_bad]) and torch.equal(got[2][~with_bad], bwd[2][~with_bad])
+    assert not torch.isfinite(got[0][with_bad]).all(2).any()
+    reached = (dot > 0) | torch.isnan(dot)
+    assert bool((~torch.isfinite(got[2]))[with_bad[:, None] & reached].all())
+    others = torch.arange(K.shape[0], device=DEV) != bad
+    assert torch.equal(got[1][others], bwd[1][others])
+
+
+@pytest.mark.parametrize("what", ["Q", "W"])
+@pytest.mark.parametrize("forward,form,q_lens,k_lens,H,d,k", NOT_FINITE)
+def test_a_query_that_is_not_a_number(forward, form, q_lens, k_lens, H, d, k, what):
+    """All its scores are NaN; other queries' scores, dQ and dW stay as they are, and so does dK of other sequences and,
+    from rows, of the keys that it does not list."""
+    b = workloads.ragged(H + k + 1, q_lens, k_lens, H=H, d=d, k=8, integer=False)
+    g = gen(k + 1)
+    lists, ds = random_lists(g, b, k), randn(g, b.n_q, k)
+    lay, Q, K, W = on_gpu(b)
+    l, e = lists.to(DEV), ds.to(DEV)
+    want = dsa.list_scores(lay, Q, K, W, l)
+    bwd = dsa.list_scores_backward(lay, Q, K, W, l, e)
+    t = q_lens[0] - 2
+    Q2, W2 = Q.clone(), W.clone()
+    if what == "Q":
+        Q2[t] = math.nan
+    else:
+        W2[t] = math.nan
+    s = scores(forward, lay, Q2, K, W2, l)
+    live = l[t] >= 0
+    assert bool(torch.isnan(s[t][live]).all()) and bool((s[t][~live] == -math.inf).all())
+    rest = torch.arange(b.n_q, device=DEV) != t
+    assert torch.equal(s[rest], want[rest])
+    got = backward(form, 1, lay, Q2, K, W2, l, e)
+    assert torch.equal(got[0][rest], bwd[0][rest]) and torch.equal(got[2][rest], bwd[2][rest])
+    listed = l[t][live].long()
+    if what == "Q":
+        assert bool(torch.isnan(got[2][t]).all()) and bool(torch.isnan(got[1][listed]).all())
+    else:
+        assert bool(torch.isnan(got[0][t]).any())
+    assert torch.equal(got[1][k_lens[0]:], bwd[1][k_lens[0]:])
+    if form == "rows":
+        others = torch.ones(K.shape[0], dtype=torch.bool, device=DEV)
+        others[listed] = False
+        assert torch.equal(got[1][others], bwd[1][others])
 
 
 def test_every_form_records_no_index_error():
