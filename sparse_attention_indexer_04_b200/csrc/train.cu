@@ -49,7 +49,7 @@ int32_t norm_bwd_ctas(int64_t n, int32_t groups, int32_t threads)
     return (int32_t)std::max<int64_t>(1, std::min((n + 8 * groups - 1) / (8 * groups), resident));
 }
 
-// The most CTAs any row group takes (narrow rows in groups of one warp or less: 256 threads).
+// The most CTAs of any backward launch: those of 128 threads.
 constexpr int64_t kNormMaxCtas = 148 * norm_bwd_per_sm(128);
 
 template <typename TX, typename TY, int VEC, int T, int NV, int NT>
@@ -94,7 +94,11 @@ dsa_status norm_pick(const NormArgs& a, bool vec, bool bwd, int32_t* np, cudaStr
     if (a.d <= 256) return norm_launch<TX, TY, 1, 32, 8, 256>(a, bwd, np, st);
     if (a.d <= 1024) return norm_launch<TX, TY, 1, 256, 4, 256>(a, bwd, np, st);
     if (a.d <= 2048) return norm_launch<TX, TY, 1, 512, 4, 512>(a, bwd, np, st);
+    // a kernel per 1024 columns, which the backward's registers count: with the 8-column one (which spills) for
+    // all from 4097 on, 4099 x 4500 fp32 100 us against 48, 4099 x 5121 104 and 68, 3000 x 7167 88 and 66
     if (a.d <= 5120) return norm_launch<TX, TY, 1, 1024, 5, 1024>(a, bwd, np, st);
+    if (a.d <= 6144) return norm_launch<TX, TY, 1, 1024, 6, 1024>(a, bwd, np, st);
+    if (a.d <= 7168) return norm_launch<TX, TY, 1, 1024, 7, 1024>(a, bwd, np, st);
     if (a.d <= 8192) return norm_launch<TX, TY, 1, 1024, 8, 1024>(a, bwd, np, st);
     return norm_launch<TX, TY, 1, 1024, 16, 1024>(a, bwd, np, st);
 }
@@ -108,8 +112,8 @@ dsa_status norm_dispatch(const NormArgs& a, int32_t tx, int32_t ty, bool vec, bo
                           : norm_pick<__nv_bfloat16, __nv_bfloat16>(a, vec, bwd, np, st);
 }
 
-// Partial sums of the weight's and bias's gradients, for the most CTAs the row count and width take:
-// 256 threads (128 to 1024 columns: 128 threads) and one row a CTA are the least.
+// Partial sums of the weight's and the bias's gradient, one row of each per CTA: norm_bwd_ctas of any row group
+// is at most one CTA per 8 rows, and kNormMaxCtas.
 size_t norm_part_floats(int64_t n, int32_t d)
 {
     return size_t(std::min<int64_t>(std::max<int64_t>(1, (n + 7) / 8), kNormMaxCtas)) * 2 * d;
