@@ -15,8 +15,8 @@
 // factor log2(e) / tau nor a sum over millions of such places may carry past fp32.
 // Bound by memory: a row is read once into registers and its gradient written once.  Exponentials
 // are base 2, one multiply and one instruction each (with expf and logf the arithmetic took as long
-// as the memory: 61.6 us for 8192 x 2048).  Rows longer than the registers of a CTA hold
-// (kDistillRegCols) are swept twice, the second time mostly from L2.
+// as the memory: 61.6 us for 8192 x 2048).  Rows that neither the registers of a CTA (kDistillRegCols) nor
+// its shared memory hold are swept twice, the second time mostly from L2.
 #pragma once
 
 #include <math_constants.h>

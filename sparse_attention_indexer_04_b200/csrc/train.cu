@@ -182,10 +182,15 @@ dsa_status distill_pick(const DistillArgs& a, cudaStream_t st)
     if (k <= 2048) return distill_launch<TT, WEIGHTS, VEC, EDGE, 128, 4 * U, 128>(a, st);
     if (k <= 4096) return distill_launch<TT, WEIGHTS, VEC, EDGE, 256, 4 * U, 256>(a, st);
     if (k <= 8192) return distill_launch<TT, WEIGHTS, VEC, EDGE, 512, 4 * U, 512>(a, st);
-    if constexpr (VEC == 4) {   // longer rows, as many as shared memory holds, read ahead
+    // longer rows, as long as shared memory holds, read ahead: 192 KB of fp32 scores and teacher are 24,576 places,
+    // with lists 16,384 (900 x 23001: 108 us in two sweeps, 68 so; 1200 x 15001 with lists: 92 us without, 69 so;
+    // 1000 x 20480: 97 and 51; 1100 x 17000: 103 and 52); few rows with lists the register form takes in less
+    // (8 x 16000: 6.3 us, 7.1 so)
+    if constexpr (VEC == 4) {
         if (k <= 12288) return distill_ring<TT, WEIGHTS, EDGE, 6, 512>(a, st);
-        if (k <= 16384 && !a.list) return distill_ring<TT, WEIGHTS, EDGE, 8, 512>(a, st);
+        if (k <= 16384 && (!a.list || a.n > 148)) return distill_ring<TT, WEIGHTS, EDGE, 8, 512>(a, st);
         if (k <= 20480 && !a.list) return distill_ring<TT, WEIGHTS, EDGE, 10, 512>(a, st);
+        if (k <= 24576 && !a.list) return distill_ring<TT, WEIGHTS, EDGE, 12, 512>(a, st);
     }
     if (k <= 16384) return distill_launch<TT, WEIGHTS, VEC, EDGE, 1024, 4 * U, 1024>(a, st);
     if (k <= kDistillRegCols) return distill_launch<TT, WEIGHTS, VEC, EDGE, 1024, 5 * U, 1024>(a, st);

@@ -118,6 +118,21 @@ def test_rows_of_any_length(k, tt, weights, lists):
                 check(a, w, e, F32, f"{name} n={n}")
 
 
+@pytest.mark.parametrize("k", [9001, 12285, 12288, 12289, 16381, 16384, 16387, 20477, 20481, 24573, 24576, 24577])
+@pytest.mark.parametrize("tt,weights,lists", [(F32, False, True), (BF, True, False), (F32, True, False)])
+def test_more_long_rows_than_the_gpu_takes_at_once(k, tt, weights, lists):
+    """A CTA's next row is read ahead while it works on one: rows on the 16-byte boundaries, and of odd strides, whose
+    end vectors are loaded on their own."""
+    n = 160
+    g = gen(k + 9)
+    s, t, l = values(g, n, k, tt, weights, lists)
+    gr = torch.randn(n, generator=g)
+    want, bound = reference(s, t, l, weights, 1.0, gr)
+    for off, pad, into in ((0, -k % 4, None), (1, 2 + k % 2, "scores"), (2, 0, None)):
+        for a, w, e, name in zip(run(s, t, l, weights, 1.0, gr, off, pad, into), want, bound, ("loss", "ds")):
+            check(a, w, e, F32, f"{name} off={off}")
+
+
 @pytest.mark.parametrize("k", [100, 513, 2048, 9001, 20000, 40000])
 @pytest.mark.parametrize("tt", [F32, BF])
 def test_masks_of_the_lowest_value(k, tt):
