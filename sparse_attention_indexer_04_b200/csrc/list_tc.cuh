@@ -223,13 +223,6 @@ struct ListTcArgs {
     const uint32_t* base;
 };
 
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // The bf16 pair (e w where s > 0, else 0) of two products s: 0 - s has its sign bit set exactly where
 // s > 0 (zeros of either sign give +0), and that bit, spread over 16 bits, masks the rounded e w.
 __device__ __forceinline__ uint32_t relu_grad_pair(float s0, float s1, uint64_t ee, uint64_t ww)

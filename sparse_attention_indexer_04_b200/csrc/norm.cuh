@@ -114,19 +114,6 @@ __device__ __forceinline__ void norm_store_vec(__nv_bfloat16* p, const float* v)
 // Arithmetic on N values in registers, two to an instruction where N is even: with one value an
 // instruction, 16-bit rows were bound by the issue of instructions (two thirds of the slots), not by
 // memory.  Every element is rounded as in the plain form.
-__device__ __forceinline__ uint64_t norm_add2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-__device__ __forceinline__ uint64_t norm_mul2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 
 // v += s
 template <int N>
@@ -135,7 +122,7 @@ __device__ __forceinline__ void norm_shift(float* v, float s)
     if constexpr (N % 2 == 0) {
         const uint64_t ss = pack_f32x2(s, s);
 #pragma unroll
-        for (int i = 0; i < N; i += 2) unpack_f32x2(norm_add2(pack_f32x2(v[i], v[i + 1]), ss), v[i], v[i + 1]);
+        for (int i = 0; i < N; i += 2) unpack_f32x2(add_f32x2(pack_f32x2(v[i], v[i + 1]), ss), v[i], v[i + 1]);
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] += s;
@@ -149,7 +136,7 @@ __device__ __forceinline__ void norm_scale(float* v, float s)
     if constexpr (N % 2 == 0) {
         const uint64_t ss = pack_f32x2(s, s);
 #pragma unroll
-        for (int i = 0; i < N; i += 2) unpack_f32x2(norm_mul2(pack_f32x2(v[i], v[i + 1]), ss), v[i], v[i + 1]);
+        for (int i = 0; i < N; i += 2) unpack_f32x2(mul_f32x2(pack_f32x2(v[i], v[i + 1]), ss), v[i], v[i + 1]);
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] *= s;
@@ -163,7 +150,7 @@ __device__ __forceinline__ void norm_times(float* v, const float* w)
     if constexpr (N % 2 == 0) {
 #pragma unroll
         for (int i = 0; i < N; i += 2)
-            unpack_f32x2(norm_mul2(pack_f32x2(v[i], v[i + 1]), pack_f32x2(w[i], w[i + 1])), v[i], v[i + 1]);
+            unpack_f32x2(mul_f32x2(pack_f32x2(v[i], v[i + 1]), pack_f32x2(w[i], w[i + 1])), v[i], v[i + 1]);
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] *= w[i];
@@ -177,7 +164,7 @@ __device__ __forceinline__ void norm_add(float* acc, const float* v)
     if constexpr (N % 2 == 0) {
 #pragma unroll
         for (int i = 0; i < N; i += 2)
-            unpack_f32x2(norm_add2(pack_f32x2(acc[i], acc[i + 1]), pack_f32x2(v[i], v[i + 1])), acc[i], acc[i + 1]);
+            unpack_f32x2(add_f32x2(pack_f32x2(acc[i], acc[i + 1]), pack_f32x2(v[i], v[i + 1])), acc[i], acc[i + 1]);
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] += v[i];
