@@ -455,14 +455,16 @@ __global__ void __launch_bounds__(NT, NT < 1024 ? norm_bwd_per_sm(NT) : 0) layer
     }
 }
 
-// Column sums of part [n_part][2][d]: 32 columns per CTA, 32 threads down each column, joined in order.
+// Column sums of part [n_part][2][d]: 32 columns per CTA, 32 threads down each column, joined in order.  Clears the
+// workspace's status words (a line in the first kernel costs 4099 x 5001 fp32, whose registers are full, 7 us).
 __global__ void __launch_bounds__(1024) layer_norm_dw_kernel(const float* part, int32_t n_part, int32_t d,
-                                                             float* dw, float* db)
+                                                             float* dw, float* db, uint32_t* status)
 {
     __shared__ float sh[32][33];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + tx;
     grid_dep_wait();
+    if (blockIdx.x == 0 && threadIdx.x < kStatusBytes / 4) status[threadIdx.x] = 0;
     float s = 0.f;
     constexpr int U = 8;   // rows read together
     if (c < 2 * d)

@@ -525,6 +525,8 @@ dsa_status dsa_layer_norm_backward(int64_t n, int32_t d, const void* dy, int32_t
         return DSA_ERR_INVALID_ARG;
     if ((s = check_ws(ws, ws_bytes, norm_ws_bytes(n, d))) != DSA_OK) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // no sums, whose kernel clears the status otherwise
+    if ((n == 0 || (!dweight && !dbias)) && cudaMemsetAsync(ws, 0, kStatusBytes, st) != cudaSuccess) return DSA_ERR_CUDA;
     if (n == 0) {   // sums over no rows
         if ((dweight && cudaMemsetAsync(dweight, 0, size_t(d) * 4, st) != cudaSuccess) ||
             (dbias && cudaMemsetAsync(dbias, 0, size_t(d) * 4, st) != cudaSuccess))
@@ -542,7 +544,7 @@ dsa_status dsa_layer_norm_backward(int64_t n, int32_t d, const void* dy, int32_t
     int32_t n_part = 0;
     if ((s = norm_dispatch(a, x_type, dy_type, vec, true, &n_part, st)) != DSA_OK || !a.part) return s;
     DSA_LAUNCH(kProfNorm, st, launch_pdl(true, layer_norm_dw_kernel, (2 * d + 31) / 32, 1024, 0, st,
-                                         (const float*)a.part, n_part, d, dweight, dbias));
+                                         (const float*)a.part, n_part, d, dweight, dbias, static_cast<uint32_t*>(ws)));
     return launched();
 }
 

@@ -31,3 +31,13 @@ def test_wide_rows(d, xt, yt):
         want, bound = ref.layer_norm_backward(dy, x, w, mean.cpu(), rstd.cpu())
         for a, v, e, t, name in zip(got, want, bound, (xt, F32, F32), ("dx", "dw", "db")):
             ref.check(a, v, e, t, f"{name} n={n}")
+
+
+@pytest.mark.parametrize("n,d", [(0, 16), (1, 16), (300, 128), (5, 5001)])
+def test_the_backward_pass_leaves_a_clear_status(n, d):
+    """Its workspace begins with a status word like every other's; what stood there is no error of this call."""
+    x = randn(gen(n + d), n, d).to(DEV)
+    _, mean, rstd = dsa.layer_norm(x, want_stats=True)
+    ws = torch.full((dsa.layer_norm_backward_workspace(n, d),), 255, dtype=torch.uint8, device=DEV)
+    dsa.layer_norm_backward(x, x, None, mean, rstd, ws=ws)
+    assert dsa.device_check(ws) == 0
