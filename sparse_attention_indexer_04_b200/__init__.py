@@ -7,6 +7,13 @@ outputs and workspaces are allocated here with torch and handed over as raw
 pointers.  There is no CPU fallback: importing this package fails loudly
 when the compiled library is missing.
 
+Calls go to the current stream, or to `stream` where one is given; its work then
+has to come after what made the arguments.  No call records autograd history:
+tensors that require a gradient are read as they are, results are detached, and
+a torch.autograd.Function of the user's joins an operator and its backward pass.
+Backward calls give all their gradients here; the C interface takes NULL for
+one that is not wanted.
+
 Entry points mirror include/dsa_index.h:
   index_scores, index_topk, index_topk_host, index_layers, pivot_group_index,
   pivot_refine_candidates, hisa_pool_keys, hisa_index, device_check, the

@@ -16,7 +16,8 @@
 //   scores 250 us: the gather, 256 bytes a listed pair out of L2 at 8.4 TB/s (tensor pipe 25 %);
 //   dQ, dW 346 us: shared memory, of whose bandwidth a tile of 128 keys takes 1150 of 1450 clocks (32 KB
 //     gathered, 48 KB read by S, 48 KB by dQ, 16 KB of G written); tensor pipe 36 %, issue 58 %;
-//   with rows 1146 us: 512 bytes a pair written, 3.7 TB/s.
+//   with rows 1146 us: 512 bytes a pair written, 3.7 TB/s (960 threads leave 64 registers each: at H = 64,
+//     d = 128 it spills 134 bytes a thread, which has not been weighed apart).
 // Roles: warp 0 and three late ones gather; warp 1 issues S, a late one dQ (and R); the warps between are
 // the epilogue, the last eight (kListGradRows) store R.  S is double-buffered, so a tile's product runs
 // while the tile before is worked on.  HP = max(16, H): heads above H have zero rows in the query tile.
