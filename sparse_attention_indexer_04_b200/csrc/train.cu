@@ -268,14 +268,16 @@ ListWork list_work(const dsa_batch* b, int32_t k)
 // Whether dK is summed from one row per listed pair or from dense products over whole key blocks.
 // Measured both ways over 35 sizes (512 to 33,000 queries, 600 to 32K keys, 1 to 512 places) with H, d of
 // 4, 32; 4, 128; 16, 64 and 64, 128, in ns: a row 0.2 at d = 128 (written by the dQ pass, read once), an empty
-// place of a tile 0.02 and as much again at d = 128; a (query, block) product 0.3 and 4.3 with 64 heads, a
-// block's CTA 150 and 350 at d = 128.  The form taken so is 0.5 % slower than the better one on average, 21 %
-// at most.
+// place of a tile 0.02 and as much again at d = 128, the bits and counts of a (query, key) 0.00005 (10 bytes for
+// 32 queries of a batch and any of its keys: 24 sequences of 4096 with 64 places and 8 heads 2.2 ms by rows, 1.7
+// dense); a (query, block) product 0.3 and 4.3 with 64 heads, a block's CTA 150 and 350 at d = 128.  The form
+// taken so is 0.5 % slower than the better one on average, 21 % at most.
 bool dk_by_rows(const dsa_batch* b, int32_t k)
 {
     const ListWork w = list_work(b, k);
     const double units = b->num_keys / kDkKeys + b->num_seqs, d = b->head_dim / 128.;
-    return w.listed * 0.2 * d + w.empty * (0.02 + 0.02 * d) <
+    const double bits = 5e-5 * b->num_queries * b->num_keys;
+    return w.listed * 0.2 * d + w.empty * (0.02 + 0.02 * d) + bits <
            w.blocks * (0.3 + 4.3 * b->num_heads / 64.) + units * (150 + 350 * d);
 }
 
